@@ -1,0 +1,644 @@
+// norm_ops.cu -- group norm with an activation over channels-last frames, and its gradient.
+//
+//   mean, rstd over an item's valid rows and a group's channels;  u = (x - mean) rstd w + b;
+//   y = act(u).                                     (formulas at the entry points in mh3a.h)
+//
+// Both directions are bound by memory: a handful of operations an element against 4 to 12 bytes.
+//
+// The general form takes any size, in passes over global memory: per-channel partial sums of a
+// chunk of rows, their combination in fixed order, then the elementwise pass.  Rows are channels
+// wide, so a warp reads whole rows (512 bytes) and every thread keeps one fixed run of V channels:
+// its statistics stay per channel in registers, and groups of any width, also ones that end inside
+// a vector, are put together only at the end.
+#include <algorithm>
+
+#include "norm_kernels.cuh"
+#include "ops_common.cuh"
+
+namespace mh3a {
+namespace norm {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 8;  // rows a thread has in flight
+
+// One block's place: item b, channel tile, row chunk.
+struct Place {
+    int b, c, ch, ty, TY;
+    bool live;  // the thread's channels exist
+};
+
+template <int V>
+__device__ __forceinline__ Place place(const NormArgs& a) {
+    Place p;
+    unsigned id = blockIdx.x;
+    p.ch = id % a.chunks;
+    id /= a.chunks;
+    const int ct = id % a.ctiles;
+    p.b = id / a.ctiles;
+    const int tx = threadIdx.x & (a.tx - 1);
+    p.ty = threadIdx.x / a.tx;
+    p.TY = kThreads / a.tx;
+    const long long c = ((long long)ct * a.tx + tx) * V;
+    p.live = c < a.C;
+    p.c = p.live ? (int)c : 0;
+    return p;
+}
+
+// Partial statistics of one channel: mean as hi + lo, and the sum of squared deviations from it.
+// Means that lie far from zero would otherwise round away what tells them apart.
+struct Stat {
+    float hi, lo, m2;
+};
+
+// Merge of two partial statistics (Chan et al.), n the count of `s`, f = nb / (n + nb).
+__device__ __forceinline__ void merge_stats(Stat& s, float n, const Stat& o, float f) {
+    const float d = (o.hi - s.hi) + (o.lo - s.lo);
+    const float t = fmaf(d, f, s.lo);
+    const float hi = s.hi + t;  // Knuth's two-sum: hi + lo = s.hi + t exactly
+    const float back = hi - s.hi;
+    s.lo = (s.hi - (hi - back)) + (t - back);
+    s.hi = hi;
+    s.m2 += o.m2 + d * d * (n * f);
+}
+
+// Per-channel statistics of one chunk of rows.  Batches of up to 8 rows are centred on their own
+// mean before they are merged, so that neither a large offset nor an outlier costs accuracy.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) k_norm_partial(const NormArgs a) {
+    ptx::grid_dep_wait();
+    const Place p = place<V>(a);
+    const int n = valid_rows(a, p.b);
+    const int r0 = min(p.ch * a.rows, n), r1 = min(r0 + a.rows, n);
+    const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c;
+    Stat st[V];
+    float cnt = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) st[i] = Stat{0.f, 0.f, 0.f};
+    if (p.live) {
+        for (int t = r0 + p.ty; t < r1; t += kBatch * p.TY) {
+            Pack<T, V> in[kBatch];
+            const int have = min(kBatch, (r1 - t + p.TY - 1) / p.TY);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (k < have) in[k] = load_pack<T, V>(x + (long long)(t + k * p.TY) * a.xr);
+            float s[V], q[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = q[i] = 0.f;
+#pragma unroll
+            for (int k = 1; k < kBatch; ++k)
+                if (k < have) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) s[i] += to_f<T>(in[k].v[i]) - to_f<T>(in[0].v[i]);
+                }
+            const float ih = 1.0f / have;
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] *= ih;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (k < have) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float d = (to_f<T>(in[k].v[i]) - to_f<T>(in[0].v[i])) - s[i];
+                        q[i] = fmaf(d, d, q[i]);
+                    }
+                }
+            const float f = have / (cnt + have);
+#pragma unroll
+            for (int i = 0; i < V; ++i) merge_stats(st[i], cnt, Stat{to_f<T>(in[0].v[i]), s[i], q[i]}, f);
+            cnt += have;
+        }
+    }
+    // lanes of a warp that share the channels
+    for (int off = 16; off >= a.tx; off >>= 1) {
+        const float nb = __shfl_xor_sync(0xffffffffu, cnt, off);
+        const float f = nb > 0.f ? nb / (cnt + nb) : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            Stat o;
+            o.hi = __shfl_xor_sync(0xffffffffu, st[i].hi, off);
+            o.lo = __shfl_xor_sync(0xffffffffu, st[i].lo, off);
+            o.m2 = __shfl_xor_sync(0xffffffffu, st[i].m2, off);
+            merge_stats(st[i], cnt, o, f);
+        }
+        cnt += nb;
+    }
+    __shared__ Stat sm[kThreads / 32][32 * V];
+    __shared__ float sn[kThreads / 32][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    sn[warp][lane] = cnt;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sm[warp][lane * V + i] = st[i];
+    __syncthreads();
+    if (warp == 0 && lane < a.tx && p.live) {
+        float4* out = reinterpret_cast<float4*>(a.ws) + ((long long)p.b * a.chunks + p.ch) * a.C + p.c;
+        for (int w = 1; w < kThreads / 32; ++w) {
+            const float nb = sn[w][lane];
+            const float f = nb > 0.f ? nb / (cnt + nb) : 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) merge_stats(st[i], cnt, sm[w][lane * V + i], f);
+            cnt += nb;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[i] = make_float4(st[i].hi, st[i].lo, st[i].m2, 0.f);
+    }
+}
+
+__device__ __forceinline__ double block_sum(double v, double* sh) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += sh[w];
+    return s;
+}
+
+// mean and rstd of one (item, group) from the chunks' statistics, in fp64.
+__global__ void __launch_bounds__(kThreads) k_norm_stats(const NormArgs a) {
+    ptx::grid_dep_wait();
+    __shared__ double sh[kThreads / 32];
+    const int b = blockIdx.x / a.G, g = blockIdx.x % a.G;
+    const int n = valid_rows(a, b);
+    const float4* part = reinterpret_cast<const float4*>(a.ws) + (long long)b * a.chunks * a.C + (long long)g * a.D;
+    const int used = a.rows > 0 ? (n + a.rows - 1) / a.rows : 0;
+    const long long m = (long long)used * a.D;
+    double s = 0;
+    for (long long i = threadIdx.x; i < m; i += kThreads) {
+        const int ch = (int)(i / a.D), c = (int)(i % a.D);
+        const int rows = min(a.rows, n - ch * a.rows);
+        const float4 v = part[(long long)ch * a.C + c];
+        s += ((double)v.x + (double)v.y) * rows;
+    }
+    const double count = (double)n * a.D;
+    const double mean = n > 0 ? block_sum(s, sh) / count : 0.0;
+    double q = 0;
+    for (long long i = threadIdx.x; i < m; i += kThreads) {
+        const int ch = (int)(i / a.D), c = (int)(i % a.D);
+        const int rows = min(a.rows, n - ch * a.rows);
+        const float4 v = part[(long long)ch * a.C + c];
+        const double d = (double)v.x + (double)v.y - mean;
+        q += (double)v.z + d * d * rows;
+    }
+    const double var = n > 0 ? block_sum(q, sh) / count : 0.0;
+    if (threadIdx.x == 0) {
+        a.mean[blockIdx.x] = (float)mean;
+        a.rstd[blockIdx.x] = (float)(1.0 / sqrt(var + (double)a.eps));
+    }
+}
+
+// y = act((x - mean) rstd w + b), zeros behind the valid rows.
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kThreads) k_norm_apply(const NormArgs a) {
+    constexpr bool kPrecise = sizeof(T) == 4;
+    ptx::grid_dep_wait();
+    const Place p = place<V>(a);
+    if (!p.live) return;
+    const int n = valid_rows(a, p.b);
+    const int r0 = min(p.ch * a.rows, a.T), r1 = min(r0 + a.rows, a.T);
+    float mu[V], sc[V], bi[V], al[V], ib[V];
+    load_param<V>(a.weight, p.c, a.C, 1.f, sc);
+    load_param<V>(a.bias, p.c, a.C, 0.f, bi);
+    if (ACT == MH3A_ACT_SNAKE_BETA) {
+        load_param<V>(a.alpha, p.c, a.C, 0.f, al);
+        load_param<V>(a.beta, p.c, a.C, 0.f, ib);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int g = p.b * a.G + min(p.c + i, a.C - 1) / a.D;
+        mu[i] = a.mean[g];
+        sc[i] *= a.rstd[g];
+        if (ACT == MH3A_ACT_SNAKE_BETA) ib[i] = 1.0f / (ib[i] + 1e-9f);
+    }
+    const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c;
+    T* y = static_cast<T*>(a.out) + (long long)p.b * a.T * a.C + p.c;
+    constexpr int U = 4;
+    for (int t = r0 + p.ty; t < r1; t += U * p.TY) {
+        Pack<T, V> in[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int row = t + k * p.TY;
+            if (row < r1 && row < n) in[k] = load_pack<T, V>(x + (long long)row * a.xr);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int row = t + k * p.TY;
+            if (row >= r1) break;
+            float f[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                f[i] = row < n ? act_fwd<ACT, kPrecise>(fmaf(to_f<T>(in[k].v[i]) - mu[i], sc[i], bi[i]),
+                                                        ACT == MH3A_ACT_SNAKE_BETA ? al[i] : 0.f,
+                                                        ACT == MH3A_ACT_SNAKE_BETA ? ib[i] : 0.f)
+                               : 0.f;
+            store_pack<T, V>(y + (long long)row * a.C, f);
+        }
+    }
+}
+
+// --------------------------------------------------------------------------------- backward
+// Sums of one channel: 0 du, 1 du xh, 2 dy * (factor of dalpha), 3 dy * (factor of dbeta).
+template <int ACT>
+constexpr int kSums = ACT == MH3A_ACT_SNAKE_BETA ? 4 : 2;
+
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kThreads) k_norm_bwd_partial(const NormArgs a) {
+    constexpr bool kPrecise = sizeof(T) == 4;
+    constexpr int NS = kSums<ACT>;
+    ptx::grid_dep_wait();
+    const Place p = place<V>(a);
+    const int n = valid_rows(a, p.b);
+    const int r0 = min(p.ch * a.rows, n), r1 = min(r0 + a.rows, n);
+    float acc[V][NS];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) acc[i][j] = 0.f;
+    if (p.live) {
+        float mu[V], rs[V], w[V], bi[V], al[V], ib[V];
+        load_param<V>(a.weight, p.c, a.C, 1.f, w);
+        load_param<V>(a.bias, p.c, a.C, 0.f, bi);
+        if (ACT == MH3A_ACT_SNAKE_BETA) {
+            load_param<V>(a.alpha, p.c, a.C, 0.f, al);
+            load_param<V>(a.beta, p.c, a.C, 0.f, ib);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int g = p.b * a.G + min(p.c + i, a.C - 1) / a.D;
+            mu[i] = a.mean[g];
+            rs[i] = a.rstd[g];
+            if (ACT == MH3A_ACT_SNAKE_BETA) ib[i] = 1.0f / (ib[i] + 1e-9f);
+        }
+        const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c;
+        const T* dy = static_cast<const T*>(a.dy) + p.b * a.gb + p.c;
+        constexpr int U = 4;
+        for (int t = r0 + p.ty; t < r1; t += U * p.TY) {
+            Pack<T, V> in[U], gr[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int row = t + k * p.TY;
+                if (row < r1) {
+                    in[k] = load_pack<T, V>(x + (long long)row * a.xr);
+                    gr[k] = load_pack<T, V>(dy + (long long)row * a.gr);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (t + k * p.TY >= r1) break;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float xh = (to_f<T>(in[k].v[i]) - mu[i]) * rs[i];
+                    const float g = to_f<T>(gr[k].v[i]);
+                    float pa = 0.f, pb = 0.f;
+                    const float du = g * act_slope<ACT, kPrecise>(fmaf(xh, w[i], bi[i]), ACT == MH3A_ACT_SNAKE_BETA ? al[i] : 0.f,
+                                                                  ACT == MH3A_ACT_SNAKE_BETA ? ib[i] : 0.f, &pa, &pb);
+                    acc[i][0] += du;
+                    acc[i][1] = fmaf(du, xh, acc[i][1]);
+                    if constexpr (NS == 4) {
+                        acc[i][2] = fmaf(g, pa, acc[i][2]);
+                        acc[i][3] = fmaf(g, pb, acc[i][3]);
+                    }
+                }
+            }
+        }
+    }
+    for (int off = 16; off >= a.tx; off >>= 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], off);
+    }
+    __shared__ float sm[kThreads / 32][32 * V * NS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) sm[warp][(i * NS + j) * 32 + lane] = acc[i][j];
+    __syncthreads();
+    if (warp == 0 && lane < a.tx && p.live) {
+        float* out = a.ws + (((long long)p.b * a.chunks + p.ch) * a.C + p.c) * NS;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                float s = 0.f;
+#pragma unroll
+                for (int w2 = 0; w2 < kThreads / 32; ++w2) s += sm[w2][(i * NS + j) * 32 + lane];
+                out[i * NS + j] = s;
+            }
+    }
+}
+
+// Per (item, channel): the chunks' sums in fixed order.  32 x 8 threads, one column of sums each.
+__global__ void __launch_bounds__(256) k_norm_bwd_sum(const NormArgs a, float* sums, int ns, int tiles) {
+    ptx::grid_dep_wait();
+    __shared__ double sh[8][33];
+    const int b = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    const long long width = (long long)a.C * ns, j = (long long)tile * 32 + lane;
+    const int n = valid_rows(a, b);
+    const int used = (n + a.rows - 1) / a.rows;
+    double s = 0;
+    if (j < width)
+        for (int ch = row; ch < used; ch += 8) s += a.ws[((long long)b * a.chunks + ch) * width + j];
+    sh[row][lane] = s;
+    __syncthreads();
+    if (row == 0 && j < width) {
+        for (int r = 1; r < 8; ++r) s += sh[r][lane];
+        sums[b * width + j] = (float)s;
+    }
+}
+
+// Warps [0, B G): the two group means of dx; blocks behind them: parameter gradients.
+__global__ void __launch_bounds__(256) k_norm_bwd_final(const NormArgs a, const float* sums, float2* means, int ns,
+                                                        int group_blocks) {
+    ptx::grid_dep_wait();
+    const int lane = threadIdx.x & 31;
+    if ((int)blockIdx.x < group_blocks) {
+        const long long bg = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+        if (bg >= (long long)a.B * a.G) return;
+        const int b = (int)(bg / a.G), g = (int)(bg % a.G);
+        double s1 = 0, s2 = 0;
+        for (int c = lane; c < a.D; c += 32) {
+            const long long ch = (long long)g * a.D + c;
+            const double w = a.weight ? (double)__ldg(a.weight + ch) : 1.0;
+            const float* s = sums + ((long long)b * a.C + ch) * ns;
+            s1 += w * s[0];
+            s2 += w * s[1];
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1) {
+            s1 += __shfl_xor_sync(0xffffffffu, s1, off);
+            s2 += __shfl_xor_sync(0xffffffffu, s2, off);
+        }
+        if (lane == 0) {
+            const int n = valid_rows(a, b);
+            const double inv = n > 0 ? 1.0 / ((double)n * a.D) : 0.0;
+            means[bg] = make_float2((float)(s1 * inv), (float)(s2 * inv));
+        }
+        return;
+    }
+    const long long c = (long long)(blockIdx.x - group_blocks) * 256 + threadIdx.x;
+    if (c >= a.C) return;
+    double s[4] = {0, 0, 0, 0};
+    for (int b = 0; b < a.B; ++b)
+        for (int j = 0; j < ns; ++j) s[j] += sums[((long long)b * a.C + c) * ns + j];
+    if (a.dbias) a.dbias[c] = (float)s[0];
+    if (a.dweight) a.dweight[c] = (float)s[1];
+    if (a.dalpha) a.dalpha[c] = (float)s[2];
+    if (a.dbeta) {
+        const double ib = 1.0 / (double)(a.beta[c] + 1e-9f);
+        a.dbeta[c] = (float)(-s[3] * ib * ib);
+    }
+}
+
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(const NormArgs a, const float2* means) {
+    constexpr bool kPrecise = sizeof(T) == 4;
+    ptx::grid_dep_wait();
+    const Place p = place<V>(a);
+    if (!p.live) return;
+    const int n = valid_rows(a, p.b);
+    const int r0 = min(p.ch * a.rows, a.T), r1 = min(r0 + a.rows, a.T);
+    float mu[V], rs[V], w[V], bi[V], al[V], ib[V], m1[V], m2[V];
+    load_param<V>(a.weight, p.c, a.C, 1.f, w);
+    load_param<V>(a.bias, p.c, a.C, 0.f, bi);
+    if (ACT == MH3A_ACT_SNAKE_BETA) {
+        load_param<V>(a.alpha, p.c, a.C, 0.f, al);
+        load_param<V>(a.beta, p.c, a.C, 0.f, ib);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int g = p.b * a.G + min(p.c + i, a.C - 1) / a.D;
+        mu[i] = a.mean[g];
+        rs[i] = a.rstd[g];
+        m1[i] = means[g].x;
+        m2[i] = means[g].y;
+        if (ACT == MH3A_ACT_SNAKE_BETA) ib[i] = 1.0f / (ib[i] + 1e-9f);
+    }
+    const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c;
+    const T* dy = static_cast<const T*>(a.dy) + p.b * a.gb + p.c;
+    T* dx = static_cast<T*>(a.out) + (long long)p.b * a.T * a.C + p.c;
+    constexpr int U = 2;
+    for (int t = r0 + p.ty; t < r1; t += U * p.TY) {
+        Pack<T, V> in[U], gr[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int row = t + k * p.TY;
+            if (row < r1 && row < n) {
+                in[k] = load_pack<T, V>(x + (long long)row * a.xr);
+                gr[k] = load_pack<T, V>(dy + (long long)row * a.gr);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int row = t + k * p.TY;
+            if (row >= r1) break;
+            float f[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                f[i] = 0.f;
+                if (row < n) {
+                    const float xh = (to_f<T>(in[k].v[i]) - mu[i]) * rs[i];
+                    float pa, pb;
+                    const float du = to_f<T>(gr[k].v[i]) *
+                                     act_slope<ACT, kPrecise>(fmaf(xh, w[i], bi[i]), ACT == MH3A_ACT_SNAKE_BETA ? al[i] : 0.f,
+                                                              ACT == MH3A_ACT_SNAKE_BETA ? ib[i] : 0.f, &pa, &pb);
+                    f[i] = rs[i] * (fmaf(du, w[i], -m1[i]) - xh * m2[i]);
+                }
+            }
+            store_pack<T, V>(dx + (long long)row * a.C, f);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------- host
+int pow2_ceil(long long n, int most) {
+    int p = 1;
+    while (p < n && p < most) p <<= 1;
+    return p;
+}
+
+// Threads, channel tiles and row chunks for vectors of V channels.  Chunks are as many as fill
+// the GPU about `waves` times over, but of at least 4 rows a thread.
+void plan_general(NormArgs* a, int V) {
+    const long long cvecs = ((long long)a->C + V - 1) / V;
+    a->tx = pow2_ceil(cvecs, 32);
+    a->ctiles = (int)((cvecs + a->tx - 1) / a->tx);
+    const int ty = kThreads / a->tx;
+    const long long want = std::max<long long>(1, 8LL * kSms / std::max<long long>(1, (long long)a->ctiles * a->B));
+    const long long most = std::max<long long>(1, ((long long)a->T + 4 * ty - 1) / (4 * ty));
+    a->chunks = (int)std::min(want, most);
+    a->rows = (a->T + a->chunks - 1) / a->chunks;
+    a->chunks = (a->T + a->rows - 1) / a->rows;
+}
+
+long long grid_general(const NormArgs& a) { return (long long)a.B * a.ctiles * a.chunks; }
+
+template <typename F, typename... Args>
+bool go(F kern, long long grid, int threads, cudaStream_t s, Args... args) {
+    return launch_dependent(kern, dim3((unsigned)grid), dim3(threads), 0, s, args...) == cudaSuccess;
+}
+
+template <typename T, int V>
+bool forward_general(const NormArgs& a, int act, cudaStream_t s) {
+    const long long grid = grid_general(a);
+    if (!go(k_norm_partial<T, V>, grid, kThreads, s, a)) return false;
+    if (!go(k_norm_stats, (long long)a.B * a.G, kThreads, s, a)) return false;
+    switch (act) {
+        case MH3A_ACT_SILU: return go(k_norm_apply<T, V, MH3A_ACT_SILU>, grid, kThreads, s, a);
+        case MH3A_ACT_SNAKE_BETA: return go(k_norm_apply<T, V, MH3A_ACT_SNAKE_BETA>, grid, kThreads, s, a);
+        default: return go(k_norm_apply<T, V, MH3A_ACT_NONE>, grid, kThreads, s, a);
+    }
+}
+
+template <typename T, int V, int ACT>
+bool backward_general(const NormArgs& a, cudaStream_t s) {
+    constexpr int NS = kSums<ACT>;
+    const long long grid = grid_general(a);
+    float* sums = a.ws + (long long)a.B * a.chunks * a.C * NS;
+    float2* means = reinterpret_cast<float2*>(sums + ((long long)a.B * a.C * NS + 3) / 4 * 4);
+    if (!go(k_norm_bwd_partial<T, V, ACT>, grid, kThreads, s, a)) return false;
+    const int tiles = (int)(((long long)a.C * NS + 31) / 32);
+    if (!go(k_norm_bwd_sum, (long long)a.B * tiles, 256, s, a, sums, NS, tiles)) return false;
+    const int gblocks = (int)(((long long)a.B * a.G + 7) / 8);
+    if (!go(k_norm_bwd_final, gblocks + (a.C + 255LL) / 256, 256, s, a, (const float*)sums, means, NS, gblocks)) return false;
+    return go(k_norm_bwd_apply<T, V, ACT>, grid, kThreads, s, a, (const float2*)means);
+}
+
+template <typename T, int V>
+bool backward_act(const NormArgs& a, int act, cudaStream_t s) {
+    switch (act) {
+        case MH3A_ACT_SILU: return backward_general<T, V, MH3A_ACT_SILU>(a, s);
+        case MH3A_ACT_SNAKE_BETA: return backward_general<T, V, MH3A_ACT_SNAKE_BETA>(a, s);
+        default: return backward_general<T, V, MH3A_ACT_NONE>(a, s);
+    }
+}
+
+int elem_bytes(int dtype) { return dtype == MH3A_DTYPE_F32 ? 4 : 2; }
+
+mh3a_status check(const mh3a_norm* p) {
+    if (!p) return MH3A_ERR_INVALID_ARG;
+    if (p->dtype < MH3A_DTYPE_F32 || p->dtype > MH3A_DTYPE_BF16) return MH3A_ERR_INVALID_ARG;
+    if (p->act < MH3A_ACT_NONE || p->act > MH3A_ACT_SNAKE_BETA) return MH3A_ERR_INVALID_ARG;
+    if (p->B < 1 || p->T < 1 || p->C < 1 || p->groups < 1 || p->C % p->groups) return MH3A_ERR_SHAPE;
+    if (p->act == MH3A_ACT_SNAKE_BETA && (!p->alpha || !p->beta)) return MH3A_ERR_INVALID_ARG;
+    // row indices plus a block's stride stay in 32 bits; grids (at most one block per item and channel)
+    // stay below 2^31
+    if (p->T > (1 << 30) || (long long)p->B * p->C >= (1LL << 31)) return MH3A_ERR_SHAPE;
+    return MH3A_OK;
+}
+
+NormArgs base_args(const mh3a_norm* p) {
+    NormArgs a{};
+    a.weight = p->weight;
+    a.bias = p->bias;
+    a.alpha = p->alpha;
+    a.beta = p->beta;
+    a.lengths = p->lengths;
+    a.B = p->B;
+    a.T = p->T;
+    a.C = p->C;
+    a.G = p->groups;
+    a.D = p->C / p->groups;
+    a.eps = p->eps;
+    return a;
+}
+
+// Scratch of the general form.  Scalar plans (V = 1) never have more chunks than vector plans
+// for the same tensor have room for, but the layouts differ, so the size is the larger of both.
+size_t general_bytes(const mh3a_norm* p, int backward) {
+    size_t most = 0;
+    for (int V : {1, 16 / elem_bytes(p->dtype)}) {
+        NormArgs a = base_args(p);
+        plan_general(&a, V);
+        const long long ns = p->act == MH3A_ACT_SNAKE_BETA ? 4 : 2;
+        long long floats = (long long)a.B * a.chunks * a.C * (backward ? ns : 4);
+        if (backward) floats += ((long long)a.B * a.C * ns + 3) / 4 * 4 + 2LL * a.B * a.G;
+        most = std::max(most, (size_t)floats * 4);
+    }
+    return (most + 255) / 256 * 256;
+}
+
+bool strides_fit(long long b, long long r, int V) { return b % V == 0 && r % V == 0; }
+
+}  // namespace norm
+}  // namespace mh3a
+
+using namespace mh3a;
+using namespace mh3a::norm;
+
+extern "C" MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward) {
+    return check(p) == MH3A_OK ? general_bytes(p, backward) : 0;
+}
+
+extern "C" MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const void* x, long long x_batch_stride,
+                                                    long long x_row_stride, void* y, float* mean, float* rstd,
+                                                    void* workspace, size_t workspace_bytes, void* stream) {
+    const mh3a_status st = check(p);
+    if (st != MH3A_OK) return st;
+    if (!x || !y || !mean || !rstd || x_batch_stride < 0 || x_row_stride < 0) return MH3A_ERR_INVALID_ARG;
+    const int e = elem_bytes(p->dtype), V = 16 / e;
+    if (!aligned(x, e) || !aligned(y, e) || !aligned(mean, 4) || !aligned(rstd, 4)) return MH3A_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < general_bytes(p, 0)) return MH3A_ERR_INVALID_ARG;
+    NormArgs a = base_args(p);
+    a.x = x;
+    a.xb = x_batch_stride;
+    a.xr = x_row_stride;
+    a.out = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.ws = static_cast<float*>(workspace);
+    const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(y, 16) && strides_fit(a.xb, a.xr, V);
+    plan_general(&a, vec ? V : 1);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    bool ok;
+    switch (p->dtype) {
+        case MH3A_DTYPE_F32: ok = vec ? forward_general<float, 4>(a, p->act, s) : forward_general<float, 1>(a, p->act, s); break;
+        case MH3A_DTYPE_F16: ok = vec ? forward_general<__half, 8>(a, p->act, s) : forward_general<__half, 1>(a, p->act, s); break;
+        default: ok = vec ? forward_general<__nv_bfloat16, 8>(a, p->act, s) : forward_general<__nv_bfloat16, 1>(a, p->act, s);
+    }
+    return ok ? MH3A_OK : launch_failed("mh3a_group_norm_act");
+}
+
+extern "C" MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p, const void* x, long long x_batch_stride,
+                                                             long long x_row_stride, const void* dy,
+                                                             long long dy_batch_stride, long long dy_row_stride,
+                                                             const float* mean, const float* rstd, void* dx,
+                                                             float* dweight, float* dbias, float* dalpha, float* dbeta,
+                                                             void* workspace, size_t workspace_bytes, void* stream) {
+    const mh3a_status st = check(p);
+    if (st != MH3A_OK) return st;
+    if (!x || !dy || !dx || !mean || !rstd) return MH3A_ERR_INVALID_ARG;
+    if (x_batch_stride < 0 || x_row_stride < 0 || dy_batch_stride < 0 || dy_row_stride < 0) return MH3A_ERR_INVALID_ARG;
+    if (p->act != MH3A_ACT_SNAKE_BETA && (dalpha || dbeta)) return MH3A_ERR_INVALID_ARG;
+    const int e = elem_bytes(p->dtype), V = 16 / e;
+    if (!aligned(x, e) || !aligned(dy, e) || !aligned(dx, e)) return MH3A_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < general_bytes(p, 1)) return MH3A_ERR_INVALID_ARG;
+    NormArgs a = base_args(p);
+    a.x = x;
+    a.xb = x_batch_stride;
+    a.xr = x_row_stride;
+    a.dy = dy;
+    a.gb = dy_batch_stride;
+    a.gr = dy_row_stride;
+    a.out = dx;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.dalpha = dalpha;
+    a.dbeta = dbeta;
+    a.ws = static_cast<float*>(workspace);
+    const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(dx, 16) &&
+                     strides_fit(a.xb, a.xr, V) && strides_fit(a.gb, a.gr, V);
+    plan_general(&a, vec ? V : 1);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    bool ok;
+    switch (p->dtype) {
+        case MH3A_DTYPE_F32: ok = vec ? backward_act<float, 4>(a, p->act, s) : backward_act<float, 1>(a, p->act, s); break;
+        case MH3A_DTYPE_F16: ok = vec ? backward_act<__half, 8>(a, p->act, s) : backward_act<__half, 1>(a, p->act, s); break;
+        default: ok = vec ? backward_act<__nv_bfloat16, 8>(a, p->act, s) : backward_act<__nv_bfloat16, 1>(a, p->act, s);
+    }
+    return ok ? MH3A_OK : launch_failed("mh3a_group_norm_act_backward");
+}

@@ -306,6 +306,69 @@ MH3A_API long long mh3a_launch_count(const mh3a_handle* h);
 /* Bytes of device memory the handle owns (weights + workspace). */
 MH3A_API long long mh3a_device_bytes(const mh3a_handle* h);
 
+/* ---------------------------------------------------------------------------------------------
+ * Operators over channels-last frames, [B, T, C] with the channels adjacent: what the layers in
+ * front of the decoder (a latent generator, an adapter, an encoder of the same family) are built
+ * of -- a normalisation with its activation, and the pointwise convolution that follows it, which
+ * is a matrix product over the B T frames.  None of them needs a handle.  They run on the current
+ * device, keep nothing between calls, allocate nothing and take their scratch memory from the
+ * caller, so calls with scratch of their own may overlap on any streams, and every call can be
+ * captured into a CUDA graph.  Results do not depend on timing: no sum is formed with atomics.
+ * ------------------------------------------------------------------------------------------- */
+typedef enum { MH3A_DTYPE_F32 = 0, MH3A_DTYPE_F16 = 1, MH3A_DTYPE_BF16 = 2 } mh3a_dtype;
+
+/* Activations, applied to the normalised value u.  MH3A_ACT_SNAKE_BETA is the decoder's SnakeBeta
+ * without its resampling: u + sin^2(alpha u) / (beta + 1e-9), linear alpha and beta per channel
+ * (alpha given twice is the plain Snake, up to the 1e-9). */
+typedef enum { MH3A_ACT_NONE = 0, MH3A_ACT_SILU = 1, MH3A_ACT_SNAKE_BETA = 2 } mh3a_activation;
+
+/* Group norm with an activation.  Channel c belongs to group c / (C / groups). */
+typedef struct {
+    int dtype;             /* mh3a_dtype of x, y, dy and dx                                  */
+    int act;               /* mh3a_activation                                                */
+    int B, T, C, groups;   /* groups divides C                                               */
+    float eps;             /* added to the variance                                          */
+    const float* weight;   /* device [C], or NULL: 1                                         */
+    const float* bias;     /* device [C], or NULL: 0                                         */
+    const float* alpha;    /* device [C], MH3A_ACT_SNAKE_BETA only                           */
+    const float* beta;     /* device [C], MH3A_ACT_SNAKE_BETA only                           */
+    const int* lengths;    /* device [B], or NULL: item b has min(max(lengths[b], 0), T)
+                              valid rows, and rows behind them take no part: they are not
+                              read, and y and dx get zeros there                             */
+} mh3a_norm;
+
+/* Scratch bytes of mh3a_group_norm_act (backward = 0) or mh3a_group_norm_act_backward
+ * (backward = 1) for *p; 0 when *p is invalid.  The size depends on *p alone. */
+MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward);
+
+/* Per item b and group g, over the item's valid rows and the group's channels:
+ *   mean, rstd = 1 / sqrt(var + eps)  (biased variance),
+ *   u = (x - mean) rstd weight_c + bias_c,   y = act(u).
+ * x: device, channels adjacent, item b and row t at x + b x_batch_stride + t x_row_stride
+ * elements (strides >= 0; 0 repeats an item or a row).  y: device [B, T, C], contiguous, must not
+ * overlap x.  mean, rstd: device [B, groups], what the backward pass needs.  An item of no valid
+ * rows has mean 0 and var 0.  All arithmetic is fp32 (combining partial statistics: fp64), rounded once to the type of y.
+ * `workspace`: device, 16-byte aligned, at least mh3a_group_norm_act_workspace(p, 0) bytes.
+ * Errors: MH3A_ERR_INVALID_ARG (NULL p, x, y, mean or rstd; unknown dtype or act; alpha or beta
+ * missing for SnakeBeta; a negative stride; a pointer not aligned to its element type;
+ * a workspace missing, too small or misaligned), MH3A_ERR_SHAPE (B, T, C or groups below 1, groups
+ * not dividing C, T above 2^30, B C of 2^31 or more), MH3A_ERR_CUDA. */
+MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const void* x, long long x_batch_stride,
+                                         long long x_row_stride, void* y, float* mean, float* rstd,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of mh3a_group_norm_act at x for the output gradient dy (strides as for x); mean and
+ * rstd are the forward pass's.  dx: device [B, T, C], contiguous, must not overlap x or dy.
+ * dweight, dbias, dalpha, dbeta: device [C] fp32, summed over all items and valid rows; each may
+ * be NULL when it is not wanted (dalpha and dbeta must be NULL unless act is
+ * MH3A_ACT_SNAKE_BETA).  Errors as mh3a_group_norm_act. */
+MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p, const void* x, long long x_batch_stride,
+                                                  long long x_row_stride, const void* dy,
+                                                  long long dy_batch_stride, long long dy_row_stride,
+                                                  const float* mean, const float* rstd, void* dx, float* dweight,
+                                                  float* dbias, float* dalpha, float* dbeta, void* workspace,
+                                                  size_t workspace_bytes, void* stream);
+
 /* Release the handle's device memory.  NULL is ignored.  Waits for the handle's work. */
 MH3A_API void mh3a_destroy(mh3a_handle* h);
 

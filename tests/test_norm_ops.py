@@ -1,0 +1,333 @@
+"""Group norm with an activation over channels-last frames, against its formulas in 64 bits."""
+import ctypes as C
+
+import pytest
+import torch
+
+import bigvgan_waveform_decoder_b200 as pkg
+from bigvgan_waveform_decoder_b200 import binding as Bd
+from bigvgan_waveform_decoder_b200 import ops
+
+from . import ops_ref as R
+
+TYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+ACTS = ("none", "silu", "snake_beta")
+
+
+def case(B, T, Cn, act, dtype, seed, offset=1.0, device="cuda"):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(B, T, Cn, generator=g) * (0.3 + 2 * torch.rand(Cn, generator=g)) + offset * torch.randn(Cn, generator=g)
+    w, b = 1 + 0.3 * torch.randn(Cn, generator=g), 0.3 * torch.randn(Cn, generator=g)
+    al, be = 0.7 + 0.6 * torch.rand(Cn, generator=g), 0.7 + 0.6 * torch.rand(Cn, generator=g)
+    if act != "snake_beta":
+        al = be = None
+    return [None if t is None else t.to(device) for t in (x.to(TYPES[dtype]), w, b, al, be)]
+
+
+def check_forward(x, groups, w, b, act, al, be, eps=1e-5, lengths=None, got=None, **kw):
+    y, mean, rstd = got or pkg.group_norm_act(x, groups, w, b, act=act, alpha=al, beta=be, eps=eps, lengths=lengths, **kw)
+    ry, rm, rr, mag = R.norm_forward(x, groups, w, b, act, al, be, eps, lengths)
+    assert y.shape == x.shape and y.dtype == x.dtype and y.is_contiguous()
+    # mean: rounded partial means put together in fp64; errors are relative to the values' size.  A batch
+    # of 8 and at most a few merges in 32 bits: under 16 roundings.
+    dev = 1 / rr
+    assert torch.all((mean.double() - rm).abs() <= 16 * R.F24 * (rm.abs() + 4 * dev))
+    # var: sums of squares of at most the same depth, two roundings a term more; rstd takes half of
+    # the variance's relative error; the shift of the mean enters squared.
+    assert torch.all((rstd.double() / rr - 1).abs() <= 32 * R.F24 * (1 + (R.F24 * rm.abs() / dev) ** 2))
+    # y: u carries the errors of mean and rstd and three roundings, at most 64 half units of its parts;
+    # the activation's slope is below 1 + alpha / beta < 3 and its own error below 2^-19 for the 16-bit
+    # hardware sine and exponential (sin^2 / beta, 2 x 2^-21 / 0.7; sigmoid times u), 2^-22 otherwise
+    own = 2.0 ** -19 if x.dtype != torch.float32 else 2.0 ** -22
+    tol = torch.finfo(x.dtype).eps / 2 * ry.abs() + 3 * 64 * R.F24 * mag + own * (1 + mag) * (act != "none")
+    tol = tol + torch.finfo(x.dtype).smallest_normal  # results below the normal range
+    bad = (y.double() - ry).abs() > tol
+    assert not bad.any(), (int(bad.sum()), float(((y.double() - ry).abs() / tol).max()))
+    return y, mean, rstd
+
+
+def check_backward(dy, x, mean, rstd, groups, w, b, act, al, be, lengths=None, got=None, **kw):
+    got = got or pkg.group_norm_act_backward(dy, x, mean, rstd, groups, w, b, act=act, alpha=al, beta=be, lengths=lengths, **kw)
+    ref, mag = R.norm_backward(dy, x, groups, w, b, act, al, be, mean, rstd, lengths)
+    assert got[0].shape == x.shape and got[0].dtype == x.dtype and got[0].is_contiguous()
+    # Every term has a few roundings and the activation's own error (2^-18 of the size of its parts for
+    # 16-bit tensors, 2^-21 for fp32: two factors of sin and cos, or u times two of the sigmoid, and u's
+    # own error times the slope's slope); a sum adds at most the depth of its longest chain, under 128
+    # values in 32 bits before the chunks are put together, of its terms' magnitudes.
+    own = 2.0 ** -18 if x.dtype != torch.float32 else 2.0 ** -21
+    d = torch.finfo(x.dtype).eps / 2 * ref["dx"].abs() + (own + 128 * R.F24) * mag["dx"] + torch.finfo(x.dtype).smallest_normal
+    bad = (got[0].double() - ref["dx"]).abs() > d
+    assert not bad.any(), (int(bad.sum()), float(((got[0].double() - ref["dx"]).abs() / d).max()))
+    for k, (name, p) in enumerate((("dweight", w), ("dbias", b), ("dalpha", al), ("dbeta", be)), 1):
+        if p is None:
+            assert got[k] is None
+            continue
+        base = mag[name] + mag["dbias"] + mag["dweight"]  # the activation's error scales with dy and u
+        off = (got[k].double() - ref[name]).abs()
+        assert torch.all(off <= (own + 128 * R.F24) * base), (name, float((off / base).max()))
+    return got
+
+
+SHAPES = [
+    # B, T, C, groups
+    (1, 1, 8, 1),         # one frame, one group
+    (1, 1, 512, 512),     # every value is a group of its own: var 0
+    (2, 4, 512, 32),      # a few frames
+    (3, 37, 24, 3),
+    (1, 5, 2048, 32),
+    (2, 33, 25, 5),       # odd width: no vector access
+    (1, 300, 7, 7),
+    (2, 500, 200, 8),     # groups that end inside a vector
+    (2, 130, 12, 4),      # 16-bit rows that are no multiple of 16 bytes
+    (2, 2000, 512, 32),
+    (3, 4097, 64, 4),
+    (1, 20011, 8, 2),     # long and narrow
+    (1, 70001, 3, 1),
+    (5, 777, 96, 1),      # one group: layer-wide statistics
+    (1, 3, 4104, 27),     # wider than a block
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward_and_backward(shape, act, dtype):
+    B, T, Cn, G = shape
+    x, w, b, al, be = case(B, T, Cn, act, dtype, seed=T + Cn)
+    _, mean, rstd = check_forward(x, G, w, b, act, al, be)
+    dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(9)).to(x.dtype).cuda()
+    check_backward(dy, x, mean, rstd, G, w, b, act, al, be)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", [(6, 50, 64, 4), (6, 900, 200, 8), (6, 4100, 32, 4), (6, 9, 25, 5), (6, 30000, 16, 2)], ids=str)
+def test_ragged_batch(shape, dtype):
+    """Rows behind an item's length take no part, whatever they hold, and come out as zeros; lengths of 0
+    and 1, and lengths outside [0, T]."""
+    B, T, Cn, G = shape
+    x, w, b, al, be = case(B, T, Cn, "snake_beta", dtype, seed=5)
+    n = torch.tensor([T, 0, 1, T // 2 + 1, -3, T + 7], dtype=torch.int32, device="cuda")
+    dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(9)).to(x.dtype).cuda()
+    for i in range(B):
+        k = min(max(int(n[i]), 0), T)
+        x[i, k:] = float("nan")
+        dy[i, k:] = float("inf")
+    y, mean, rstd = check_forward(x, G, w, b, "snake_beta", al, be, lengths=n)
+    got = check_backward(dy, x, mean, rstd, G, w, b, "snake_beta", al, be, lengths=n)
+    for i in range(B):
+        k = min(max(int(n[i]), 0), T)
+        assert torch.all(y[i, k:] == 0) and torch.all(got[0][i, k:] == 0)
+    assert torch.all(mean[[1, 4]] == 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("T", (40, 3000, 60000))
+def test_strided_and_repeated_rows(T, dtype):
+    """Inputs that are slices, transposed batches or repeated items; outputs are contiguous."""
+    Cn, G = 32, 4
+    x, w, b, al, be = case(1, 3 * T, 2 * Cn, "silu", dtype, seed=2)
+    wide = x.view(3, T, 2 * Cn)
+    w, b = w[:Cn].contiguous(), b[:Cn].contiguous()
+    views = [wide[:, :, Cn:], wide.view(T, 3, 2 * Cn).transpose(0, 1)[..., :Cn], wide[:1, :, :Cn].expand(3, T, Cn),
+             wide[:, :, 1:Cn + 1]]
+    for v in views:
+        _, mean, rstd = check_forward(v, G, w, b, "silu", None, None)
+        check_backward(v, v.flip(0) if v.stride(0) else v, mean, rstd, G, w, b, "silu", None, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", (7, 2500, 50000))
+def test_far_offset_and_outliers(T):
+    """Statistics of values that lie far from zero, or that one value outweighs."""
+    Cn, G = 32, 4
+    x, w, b, _, _ = case(2, T, Cn, "none", "fp32", seed=3)
+    check_forward(x + 1000, G, w, b, "none", None, None)
+    x[:, 0] = 3e4
+    check_forward(x, G, w, b, "none", None, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", (7, 2500, 50000))
+def test_not_finite_values_stay_in_their_group(T):
+    Cn, G = 32, 4
+    x, w, b, al, be = case(2, T, Cn, "snake_beta", "bf16", seed=4)
+    y0, m0, r0 = pkg.group_norm_act(x, G, w, b, act="snake_beta", alpha=al, beta=be)
+    x[0, T // 2, 3] = float("inf")
+    x[1, T - 1, 31] = float("nan")
+    y, m, r = pkg.group_norm_act(x, G, w, b, act="snake_beta", alpha=al, beta=be)
+    hit = torch.zeros(2, G, dtype=torch.bool, device="cuda")
+    hit[0, 0] = hit[1, 3] = True
+    assert torch.all(torch.isnan(y.view(2, T, G, 8).float()).any(dim=3).all(dim=1) | ~hit)
+    keep = ~hit[:, None, :, None].expand(2, T, G, 8)
+    assert torch.equal(y.view(2, T, G, 8)[keep], y0.view(2, T, G, 8)[keep])
+    assert torch.equal(m[~hit], m0[~hit]) and torch.equal(r[~hit], r0[~hit])
+
+
+@pytest.mark.gpu
+def test_without_parameters_and_with_some():
+    x, w, b, al, be = case(2, 60, 48, "snake_beta", "fp32", seed=6)
+    dy = torch.randn_like(x)
+    for ww, bb in ((None, None), (w, None), (None, b)):
+        _, mean, rstd = check_forward(x, 6, ww, bb, "snake_beta", al, be)
+        check_backward(dy, x, mean, rstd, 6, ww, bb, "snake_beta", al, be)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T", (6, 1100))
+def test_gradient_against_differences(act, T):
+    """Central differences of sum(y dy) along random directions, in fp32 with the reference's forward in
+    64 bits: the analytic gradients have to give the same slopes."""
+    G = 4
+    x, w, b, al, be = case(2, T, 16, act, "fp32", seed=7)
+    dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(1)).cuda()
+    _, mean, rstd = pkg.group_norm_act(x, G, w, b, act=act, alpha=al, beta=be)
+    got = pkg.group_norm_act_backward(dy, x, mean, rstd, G, w, b, act=act, alpha=al, beta=be)
+    params = [x, w, b, al, be]
+    for k, (p, grad) in enumerate(zip(params, got)):
+        if p is None:
+            continue
+        d = torch.randn(p.shape, generator=torch.Generator().manual_seed(k)).cuda().double()
+        h = 1e-5
+
+        def loss(sign):
+            q = [None if t is None else t.double() for t in params]
+            q[k] = q[k] + sign * h * d
+            return float((R.norm_forward(q[0], G, q[1], q[2], act, q[3], q[4], 1e-5, None)[0] * dy.double()).sum())
+
+        slope = (loss(1) - loss(-1)) / (2 * h)
+        have = float((grad.double() * d).sum())
+        size = float((grad.double() * d).abs().sum())
+        # the difference is off by h^2 times a third derivative of order 10 (1e-9) and by rounding in 64
+        # bits (1e-16 x sum |y dy| / h); the gradient by a few 2^-21 of its parts
+        assert abs(slope - have) <= 2e-6 * size + 1e-6 * x.numel() ** 0.5, (k, slope, have, size)
+
+
+@pytest.mark.gpu
+def test_repeats_are_identical_and_streams_do_not_mix():
+    x, w, b, al, be = case(3, 3001, 64, "snake_beta", "bf16", seed=8)
+    x2 = x.flip(0).contiguous()
+    dy = torch.randn(x.shape, device="cuda").to(x.dtype)
+    kw = dict(act="snake_beta", alpha=al, beta=be)
+
+    def both(x, stream=None):
+        y, m, r = pkg.group_norm_act(x, 8, w, b, stream=stream, **kw)
+        return (y, m, r) + pkg.group_norm_act_backward(dy, x, m, r, 8, w, b, stream=stream, **kw)
+
+    first, second = both(x), both(x2)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    runs = []
+    for _ in range(5):
+        runs.append((both(x, s1), both(x2, s2.cuda_stream)))
+    torch.cuda.synchronize()
+    for a, c in runs:
+        assert all(torch.equal(p, q) for p, q in zip(a, first))
+        assert all(torch.equal(p, q) for p, q in zip(c, second))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", (5, 3000))
+def test_captured_and_replayed(T):
+    x, w, b, al, be = case(2, T, 64, "snake_beta", "fp32", seed=10)
+    dy = torch.randn_like(x)
+    kw = dict(act="snake_beta", alpha=al, beta=be)
+    graphs, outs = [], []
+    for k in range(2):  # two graphs with scratch of their own, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y, m, r = pkg.group_norm_act(x, 8, w, b, **kw)
+            outs.append((y, m, r) + pkg.group_norm_act_backward(dy, x, m, r, 8, w, b, **kw))
+        graphs.append(g)
+    x.copy_(x.flip(1).clone() * 1.5)
+    for g in (graphs[0], graphs[1], graphs[0]):
+        g.replay()
+    torch.cuda.synchronize()
+    y, m, r = pkg.group_norm_act(x, 8, w, b, **kw)
+    ref = (y, m, r) + pkg.group_norm_act_backward(dy, x, m, r, 8, w, b, **kw)
+    for o in outs:
+        assert all(torch.equal(p, q) for p, q in zip(o, ref))
+
+
+@pytest.mark.gpu
+def test_writes_nothing_outside_its_outputs():
+    """Guard values around y, dx and the statistics stay; a caller's `out` is used."""
+    B, T, Cn, G = 2, 301, 24, 3
+    x, w, b, _, _ = case(B, T, Cn, "silu", "bf16", seed=11)
+    buf = torch.full((x.numel() + 64,), 7.0, device="cuda", dtype=x.dtype)
+    out = buf[32:32 + x.numel()].view(B, T, Cn)
+    y, m, r = pkg.group_norm_act(x, G, w, b, act="silu", out=out)
+    assert y.data_ptr() == out.data_ptr()
+    check_forward(x, G, w, b, "silu", None, None, got=(y, m, r))
+    assert torch.all(buf[:32] == 7) and torch.all(buf[-32:] == 7)
+
+
+@pytest.mark.gpu
+def test_python_refusals():
+    x, w, b, al, be = case(2, 10, 24, "snake_beta", "fp32", seed=12)
+    f, n = pkg.group_norm_act, pkg.MH3AError
+    for bad in (lambda: f(x, 5, w, b), lambda: f(x, 0, w, b), lambda: f(x, 3, w[:8], b), lambda: f(x, 3, w.cpu(), b),
+                lambda: f(x, 3, w.half(), b), lambda: f(x.cpu(), 3, w, b), lambda: f(x.double(), 3, w, b),
+                lambda: f(x[0], 3, w, b), lambda: f(x[:, :, ::2], 3), lambda: f(x[:, :0], 3), lambda: f(x, 3, act="gelu"),
+                lambda: f(x, 3, act="snake_beta"), lambda: f(x, 3, act="silu", alpha=al, beta=be),
+                lambda: f(x, 3, act="snake_beta", alpha=al), lambda: f(x, 3, lengths=torch.tensor([1, 2])),
+                lambda: f(x, 3, lengths=torch.tensor([1, 2], device="cuda")),
+                lambda: f(x, 3, lengths=torch.tensor([1], device="cuda", dtype=torch.int32)),
+                lambda: f(x, 3, out=torch.empty(2, 10, 12, device="cuda")), lambda: f(x, 3, out=x.half())):
+        with pytest.raises(n):
+            bad()
+    y, m, r = f(x, 3)
+    g = pkg.group_norm_act_backward
+    for bad in (lambda: g(y[:1], x, m, r, 3), lambda: g(y.half(), x, m, r, 3), lambda: g(y, x, m[:1], r, 3),
+                lambda: g(y, x, m, r.double(), 3), lambda: g(y, x, m, r, 4)):
+        with pytest.raises(n):
+            bad()
+
+
+def norm(**kw):
+    p = ops.mh3a_norm(1, 1, 2, 10, 24, 3, 1e-5, None, None, None, None, None)
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return p
+
+
+def test_abi_refusals():
+    """Every refusal comes before any device work (the pointers here are no device memory)."""
+    L = ops._load()
+    p0, ok = C.byref(norm()), 1 << 20
+    size = L.mh3a_group_norm_act_workspace(p0, 0)
+    assert size > 0 and L.mh3a_group_norm_act_workspace(p0, 1) >= size
+
+    def fwd(p=None, x=ok, xb=240, xr=24, y=ok, mean=ok, rstd=ok, ws=ok, n=size):
+        return L.mh3a_group_norm_act(None if p is None else C.byref(p), x, xb, xr, y, mean, rstd, ws, n, None)
+
+    good = norm()
+    assert fwd(None) == 1
+    for kw in (dict(x=None), dict(y=None), dict(mean=None), dict(rstd=None), dict(ws=None), dict(n=size - 1), dict(xb=-1),
+               dict(xr=-1), dict(x=ok + 1), dict(y=ok + 1), dict(ws=ok + 8)):
+        assert fwd(good, **kw) == 1, kw
+    for kw in (dict(dtype=3), dict(dtype=-1), dict(act=3), dict(act=-1), dict(act=2), dict(act=2, alpha=ok)):
+        assert fwd(norm(**kw)) == 1, kw
+        assert L.mh3a_group_norm_act_workspace(C.byref(norm(**kw)), 0) == 0
+    for kw in (dict(B=0), dict(T=0), dict(C=0), dict(groups=0), dict(groups=5), dict(T=(1 << 30) + 1),
+               dict(B=1 << 20, C=1 << 12, groups=1)):
+        assert fwd(norm(**kw)) == 3, kw
+    n1 = L.mh3a_group_norm_act_workspace(p0, 1)
+
+    def bwd(p=None, x=ok, dy=ok, mean=ok, rstd=ok, dx=ok, da=None, ws=ok, n=n1, gb=240):
+        return L.mh3a_group_norm_act_backward(None if p is None else C.byref(p), x, 240, 24, dy, gb, 24, mean, rstd, dx, ok, ok,
+                                              da, None, ws, n, None)
+
+    assert bwd(None) == 1
+    for kw in (dict(x=None), dict(dy=None), dict(mean=None), dict(rstd=None), dict(dx=None), dict(da=ok), dict(ws=None),
+               dict(n=n1 - 1), dict(gb=-1), dict(dy=ok + 1)):
+        assert bwd(good, **kw) == 1, kw
+    assert bwd(norm(groups=7)) == 3
+    assert L.mh3a_group_norm_act_workspace(None, 0) == 0
+
+
+def test_exports():
+    assert {"mh3a_group_norm_act", "mh3a_group_norm_act_backward", "mh3a_group_norm_act_workspace"} <= set(Bd.EXPORTS)
