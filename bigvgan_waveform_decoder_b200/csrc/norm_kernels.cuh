@@ -70,6 +70,19 @@ __device__ __forceinline__ void unpack(const Pack<T, V>& p, float (&f)[V]) {
     for (int i = 0; i < V; ++i) f[i] = to_f<T>(p.v[i]);
 }
 
+// Pairs of neighbouring elements, for the packed fp32x2 instructions.
+__device__ __forceinline__ float2 pair_of(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ float2 pair_of(const __half* v) { return __half22float2(*reinterpret_cast<const __half2*>(v)); }
+__device__ __forceinline__ float2 pair_of(const __nv_bfloat16* v) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(v);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack_pairs(const Pack<T, V>& p, float2 (&f)[V / 2]) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f[i] = pair_of(p.v + 2 * i);
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void store_pack(T* p, const float (&f)[V]) {
     Pack<T, V> o;

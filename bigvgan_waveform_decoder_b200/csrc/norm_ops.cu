@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "norm_kernels.cuh"
+#include "norm_resident.cuh"
 #include "ops_common.cuh"
 
 namespace mh3a {
@@ -480,6 +481,76 @@ bool go(F kern, long long grid, int threads, cudaStream_t s, Args... args) {
     return launch_dependent(kern, dim3((unsigned)grid), dim3(threads), 0, s, args...) == cudaSuccess;
 }
 
+// Shared memory of a resident block: two blocks an SM where the slab allows, else one.
+constexpr int kResTwo = 112 * 1024, kResOne = 224 * 1024;
+
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
+// Divides a tensor for the resident form; false where one cluster cannot hold an item's slab.
+// Slabs are whole groups and whole vectors.  `bytes_row` are kept per channel and row (x, or x and
+// dy), `extra(nt, W)` beside them.
+template <typename Extra>
+bool plan_resident(const NormArgs& a, int V, int e, int bytes_row, Extra extra, Resident* r, int* threads) {
+    const int unit = a.D / gcd(a.D, V) * V;
+    const int units = a.C / unit;
+    for (int want : {128, 64, 32}) {
+        int k = 1;
+        while (k < units && (units % k || k * unit * e < want)) ++k;
+        const int W = k * unit;
+        const int slabs = a.C / W;
+        // more blocks than this leave SMs idle no longer
+        if (want == 128 && k > 1 && (long long)a.B * slabs * 8 < 2 * kSms && a.T >= 128) continue;
+        for (int limit : {kResTwo, kResOne}) {
+            for (int nt : {256, 512}) {
+                if (W / V > nt) continue;
+                auto bytes = [&](int s) { return (long long)((a.T + s - 1) / s) * W * bytes_row + extra(nt, W); };
+                int S = 1;
+                while (S < 16 && bytes(S) > limit) S *= 2;
+                if (bytes(S) > limit) continue;
+                while (S < 8 && (long long)a.B * slabs * S * 2 <= 2 * kSms && (a.T + 2 * S - 1) / (2 * S) >= 16) S *= 2;
+                const int rows = (a.T + S - 1) / S;
+                // 512 threads once a thread of 256 would have more than 16 rows
+                if (nt == 256 && (long long)rows * (W / V) > 16 * 256 && W / V <= 512) continue;
+                *r = Resident{S, rows, W, slabs, (int)bytes(S)};
+                *threads = nt;
+                return true;
+            }
+        }
+    }
+    return false;
+}
+
+template <typename K, typename... Args>
+bool go_resident(K kern, const NormArgs& a, const Resident& r, int threads, cudaStream_t s, Args... args) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kResOne) != cudaSuccess) return false;
+    if (r.S > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((long long)a.B * r.slabs * r.S));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = r.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = r.S;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a, r, args...) == cudaSuccess;
+}
+
+template <typename T, int V, int ACT, int NT>
+bool forward_resident(const NormArgs& a, const Resident& r, cudaStream_t s) {
+    return a.D % V == 0 ? go_resident(k_norm_resident<T, V, ACT, true, NT>, a, r, NT, s)
+                        : go_resident(k_norm_resident<T, V, ACT, false, NT>, a, r, NT, s);
+}
+
+template <typename T, int V, int ACT>
+bool forward_resident(const NormArgs& a, const Resident& r, int threads, cudaStream_t s) {
+    return threads == 256 ? forward_resident<T, V, ACT, 256>(a, r, s) : forward_resident<T, V, ACT, 512>(a, r, s);
+}
+
 template <typename T, int V>
 bool forward_general(const NormArgs& a, int act, cudaStream_t s) {
     const long long grid = grid_general(a);
@@ -490,6 +561,23 @@ bool forward_general(const NormArgs& a, int act, cudaStream_t s) {
         case MH3A_ACT_SNAKE_BETA: return go(k_norm_apply<T, V, MH3A_ACT_SNAKE_BETA>, grid, kThreads, s, a);
         default: return go(k_norm_apply<T, V, MH3A_ACT_NONE>, grid, kThreads, s, a);
     }
+}
+
+template <typename T>
+bool forward(NormArgs& a, int act, bool vec, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    Resident r;
+    int nt;
+    auto extra = [&](int threads, int W) { return res_fwd_extra(threads, W, a.D, V); };
+    if (vec && plan_resident(a, V, sizeof(T), sizeof(T), extra, &r, &nt)) {
+        switch (act) {
+            case MH3A_ACT_SILU: return forward_resident<T, V, MH3A_ACT_SILU>(a, r, nt, s);
+            case MH3A_ACT_SNAKE_BETA: return forward_resident<T, V, MH3A_ACT_SNAKE_BETA>(a, r, nt, s);
+            default: return forward_resident<T, V, MH3A_ACT_NONE>(a, r, nt, s);
+        }
+    }
+    plan_general(&a, vec ? V : 1);
+    return vec ? forward_general<T, V>(a, act, s) : forward_general<T, 1>(a, act, s);
 }
 
 template <typename T, int V, int ACT>
@@ -590,13 +678,12 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const vo
     a.rstd = rstd;
     a.ws = static_cast<float*>(workspace);
     const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(y, 16) && strides_fit(a.xb, a.xr, V);
-    plan_general(&a, vec ? V : 1);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     bool ok;
     switch (p->dtype) {
-        case MH3A_DTYPE_F32: ok = vec ? forward_general<float, 4>(a, p->act, s) : forward_general<float, 1>(a, p->act, s); break;
-        case MH3A_DTYPE_F16: ok = vec ? forward_general<__half, 8>(a, p->act, s) : forward_general<__half, 1>(a, p->act, s); break;
-        default: ok = vec ? forward_general<__nv_bfloat16, 8>(a, p->act, s) : forward_general<__nv_bfloat16, 1>(a, p->act, s);
+        case MH3A_DTYPE_F32: ok = forward<float>(a, p->act, vec, s); break;
+        case MH3A_DTYPE_F16: ok = forward<__half>(a, p->act, vec, s); break;
+        default: ok = forward<__nv_bfloat16>(a, p->act, vec, s);
     }
     return ok ? MH3A_OK : launch_failed("mh3a_group_norm_act");
 }
