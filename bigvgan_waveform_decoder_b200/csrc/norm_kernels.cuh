@@ -83,11 +83,32 @@ __device__ __forceinline__ void unpack_pairs(const Pack<T, V>& p, float2 (&f)[V 
     for (int i = 0; i < V / 2; ++i) f[i] = pair_of(p.v + 2 * i);
 }
 
+__device__ __forceinline__ void put_pair(float* v, float2 f) { *reinterpret_cast<float2*>(v) = f; }
+__device__ __forceinline__ void put_pair(__half* v, float2 f) {
+    *reinterpret_cast<__half2*>(v) = __floats2half2_rn(f.x, f.y);
+}
+__device__ __forceinline__ void put_pair(__nv_bfloat16* v, float2 f) {
+    *reinterpret_cast<__nv_bfloat162*>(v) = __floats2bfloat162_rn(f.x, f.y);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T* p, const float2 (&f)[V / 2]) {
+    Pack<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) put_pair(o.v + 2 * i, f[i]);
+    *reinterpret_cast<Pack<T, V>*>(p) = o;
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void store_pack(T* p, const float (&f)[V]) {
     Pack<T, V> o;
+    if constexpr (V % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) o.v[i] = from_f<T>(f[i]);
+        for (int i = 0; i < V; i += 2) put_pair(o.v + i, make_float2(f[i], f[i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o.v[i] = from_f<T>(f[i]);
+    }
     *reinterpret_cast<Pack<T, V>*>(p) = o;
 }
 
@@ -98,19 +119,43 @@ __device__ __forceinline__ void load_param(const float* p, int c, int C, float o
     for (int i = 0; i < V; ++i) f[i] = (p && c + i < C) ? __ldg(p + c + i) : other;
 }
 
+// The same for a whole vector, by 16-byte loads: c is a multiple of V, C too, p 16-byte aligned.
+template <int V>
+__device__ __forceinline__ void load_param_vec(const float* p, int c, float other, float2 (&f)[V / 2]) {
+    if (p) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p + c) + i);
+            f[2 * i] = make_float2(v.x, v.y);
+            f[2 * i + 1] = make_float2(v.z, v.w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) f[i] = make_float2(other, other);
+    }
+}
+
+// n / d by a multiplication: mul = ceil(2^32 / d) gives the exact quotient for n d < 2^32, which
+// holds for thread indices and for channels of one slab.
+struct FastDiv {
+    unsigned d, mul;
+};
+__device__ __forceinline__ unsigned operator/(unsigned n, FastDiv f) { return f.d == 1 ? n : __umulhi(n, f.mul); }
+
 // sin(theta) and cos(theta) up to a common sign, theta = alpha u: what sin^2 and sin cos need, both
-// of period pi.  The phase is reduced to [-pi/2, pi/2] by the Cody-Waite method (pi as fp32(pi)
-// plus the fp32 remainder, the product's rounding error carried along from one fma).  fp32 tensors
-// take the Taylor series there (truncated terms below 7e-10); 16-bit tensors take the hardware
-// sine, whose 2^-21 absolute error is far below their rounding.
+// of period pi.  fp32 tensors: the phase is reduced to [-pi/2, pi/2] by the Cody-Waite method (pi as
+// fp32(pi) plus the fp32 remainder, the product's rounding error carried along from one fma), then
+// the Taylor series (truncated terms below 7e-10).  16-bit tensors: the hardware sine, whose 2^-21
+// absolute error is far below their rounding; its argument loses |theta| 2^-24 as the product itself
+// does, so a reduction first would gain nothing.
 template <bool PRECISE>
 __device__ __forceinline__ void sin_cos_mod_pi(float alpha, float u, float* sn, float* cs) {
     const float v = alpha * u;
-    const float e = fmaf(alpha, u, -v);
-    const float k = rintf(v * 0.318309886183790671538f);
-    float r = fmaf(-k, 3.14159274101257324219f, v);
-    r = fmaf(-k, -8.74227800037248297e-08f, r) + e;
     if (PRECISE) {
+        const float e = fmaf(alpha, u, -v);
+        const float k = rintf(v * 0.318309886183790671538f);
+        float r = fmaf(-k, 3.14159274101257324219f, v);
+        r = fmaf(-k, -8.74227800037248297e-08f, r) + e;
         const float r2 = r * r;
         float p = 1.0f / 6227020800.0f;
         p = fmaf(p, r2, -1.0f / 39916800.0f);
@@ -128,15 +173,28 @@ __device__ __forceinline__ void sin_cos_mod_pi(float alpha, float u, float* sn, 
         q = fmaf(q, r2, -0.5f);
         *cs = fmaf(q, r2, 1.0f);
     } else {
-        *sn = __sinf(r);
-        *cs = __cosf(r);
+        *sn = __sinf(v);
+        *cs = __cosf(v);
     }
 }
 
+__device__ __forceinline__ float ex2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + e^-u).  16-bit tensors take the hardware's exponential and reciprocal (each a few ulp;
+// results below 2^-126 become 0), without the scaling that keeps subnormal numbers.
 template <bool PRECISE>
 __device__ __forceinline__ float sigmoid(float u) {
     if (PRECISE) return 1.0f / (1.0f + expf(-u));
-    return __fdividef(1.0f, 1.0f + __expf(-u));
+    return rcp_ftz(1.0f + ex2_ftz(-1.44269504088896341f * u));
 }
 
 // y = act(u); ib = 1 / (beta + 1e-9)
@@ -149,6 +207,21 @@ __device__ __forceinline__ float act_fwd(float u, float al, float ib) {
         return fmaf(sn * sn, ib, u);
     }
     return u;
+}
+
+// The same for a pair, by packed fp32x2 operations.
+template <int ACT, bool PRECISE>
+__device__ __forceinline__ float2 act_fwd2(float2 u, float2 al, float2 ib) {
+    if (PRECISE || ACT == MH3A_ACT_NONE)
+        return make_float2(act_fwd<ACT, PRECISE>(u.x, al.x, ib.x), act_fwd<ACT, PRECISE>(u.y, al.y, ib.y));
+    if (ACT == MH3A_ACT_SILU) {
+        const float2 t = __fmul2_rn(u, make_float2(-1.44269504088896341f, -1.44269504088896341f));
+        const float2 e = __fadd2_rn(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), make_float2(1.f, 1.f));
+        return __fmul2_rn(u, make_float2(rcp_ftz(e.x), rcp_ftz(e.y)));
+    }
+    const float2 v = __fmul2_rn(al, u);
+    const float2 sn = make_float2(__sinf(v.x), __sinf(v.y));
+    return __ffma2_rn(__fmul2_rn(sn, sn), ib, u);
 }
 
 // act'(u), and for SnakeBeta the factors of dalpha and dbeta: dalpha = sum dy *pa,

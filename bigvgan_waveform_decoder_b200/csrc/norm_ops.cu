@@ -29,9 +29,8 @@ struct Place {
 };
 
 template <int V>
-__device__ __forceinline__ Place place(const NormArgs& a) {
+__device__ __forceinline__ Place place(const NormArgs& a, unsigned id) {
     Place p;
-    unsigned id = blockIdx.x;
     p.ch = id % a.chunks;
     id /= a.chunks;
     const int ct = id % a.ctiles;
@@ -62,51 +61,87 @@ __device__ __forceinline__ void merge_stats(Stat& s, float n, const Stat& o, flo
     s.m2 += o.m2 + d * d * (n * f);
 }
 
-// Per-channel statistics of one chunk of rows.  Batches of up to 8 rows are centred on their own
-// mean before they are merged, so that neither a large offset nor an outlier costs accuracy.
+// Adds up V values of a row (as pairs where V is even).
+template <int V>
+struct Acc {
+    static constexpr int H = V == 1 ? 1 : V / 2;
+    float2 v[H];
+};
+template <typename T, int V>
+__device__ __forceinline__ void unpack_acc(const Pack<T, V>& p, Acc<V>& f) {
+    if constexpr (V == 1) f.v[0] = make_float2(to_f<T>(p.v[0]), 0.f);
+    else unpack_pairs<T, V>(p, f.v);
+}
+
+// Per-channel statistics of one chunk of rows.  A thread adds up deviations from the mean of its
+// first 8 rows, so neither a large offset nor an outlier (which moves that mean by an eighth) costs
+// accuracy; threads, warps and chunks are merged as (mean, squared deviations).
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) k_norm_partial(const NormArgs a) {
+    constexpr int H = Acc<V>::H;
     ptx::grid_dep_wait();
-    const Place p = place<V>(a);
+    ptx::grid_dep_launch();
+    const Place p = place<V>(a, blockIdx.x);
     const int n = valid_rows(a, p.b);
     const int r0 = min(p.ch * a.rows, n), r1 = min(r0 + a.rows, n);
-    const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c;
+    const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c + (long long)(r0 + p.ty) * a.xr;
+    const long long step = (long long)p.TY * a.xr;
+    const int mine = p.live && r1 - r0 > p.ty ? (r1 - r0 - p.ty + p.TY - 1) / p.TY : 0;
+    Acc<V> sh, s, q;
+#pragma unroll
+    for (int i = 0; i < H; ++i) sh.v[i] = s.v[i] = q.v[i] = make_float2(0.f, 0.f);
+    auto add = [&](const Pack<T, V>& in) {
+        Acc<V> f;
+        unpack_acc<T, V>(in, f);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float2 d = __fadd2_rn(f.v[i], sh.v[i]);
+            s.v[i] = __fadd2_rn(s.v[i], d);
+            q.v[i] = __ffma2_rn(d, d, q.v[i]);
+        }
+    };
+    Pack<T, V> in[kBatch];
+    for (int k0 = 0; k0 < mine; k0 += kBatch) {
+        const int have = min(kBatch, mine - k0);
+        if (have == kBatch) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) in[k] = load_pack<T, V>(x + k * step);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (k < have) in[k] = load_pack<T, V>(x + k * step);
+        }
+        x += kBatch * step;
+        if (k0 == 0) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (k < have) {
+                    Acc<V> f;
+                    unpack_acc<T, V>(in[k], f);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) sh.v[i] = __fadd2_rn(sh.v[i], f.v[i]);
+                }
+            const float f = -1.0f / have;
+#pragma unroll
+            for (int i = 0; i < H; ++i) sh.v[i] = __fmul2_rn(sh.v[i], make_float2(f, f));
+        }
+        if (have == kBatch) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) add(in[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (k < have) add(in[k]);
+        }
+    }
+    float cnt = (float)mine;
     Stat st[V];
-    float cnt = 0.f;
+    {
+        const float ic = mine > 0 ? 1.0f / cnt : 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) st[i] = Stat{0.f, 0.f, 0.f};
-    if (p.live) {
-        for (int t = r0 + p.ty; t < r1; t += kBatch * p.TY) {
-            Pack<T, V> in[kBatch];
-            const int have = min(kBatch, (r1 - t + p.TY - 1) / p.TY);
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (k < have) in[k] = load_pack<T, V>(x + (long long)(t + k * p.TY) * a.xr);
-            float s[V], q[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) s[i] = q[i] = 0.f;
-#pragma unroll
-            for (int k = 1; k < kBatch; ++k)
-                if (k < have) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) s[i] += to_f<T>(in[k].v[i]) - to_f<T>(in[0].v[i]);
-                }
-            const float ih = 1.0f / have;
-#pragma unroll
-            for (int i = 0; i < V; ++i) s[i] *= ih;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (k < have) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float d = (to_f<T>(in[k].v[i]) - to_f<T>(in[0].v[i])) - s[i];
-                        q[i] = fmaf(d, d, q[i]);
-                    }
-                }
-            const float f = have / (cnt + have);
-#pragma unroll
-            for (int i = 0; i < V; ++i) merge_stats(st[i], cnt, Stat{to_f<T>(in[0].v[i]), s[i], q[i]}, f);
-            cnt += have;
+        for (int i = 0; i < H; ++i) {
+            st[V == 1 ? 0 : 2 * i] = Stat{-sh.v[i].x, s.v[i].x * ic, q.v[i].x - s.v[i].x * s.v[i].x * ic};
+            if constexpr (V > 1) st[2 * i + 1] = Stat{-sh.v[i].y, s.v[i].y * ic, q.v[i].y - s.v[i].y * s.v[i].y * ic};
         }
     }
     // lanes of a warp that share the channels
@@ -188,53 +223,58 @@ __global__ void __launch_bounds__(kThreads) k_norm_stats(const NormArgs a) {
     }
 }
 
-// y = act((x - mean) rstd w + b), zeros behind the valid rows.
+// y = act((x - mean) rstd w + b), zeros behind the valid rows.  Blocks go through the tensor from its
+// end: what the statistics pass read last is still in L2.
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads) k_norm_apply(const NormArgs a) {
-    constexpr bool kPrecise = sizeof(T) == 4;
+    constexpr bool kPrecise = sizeof(T) == 4, kSnake = ACT == MH3A_ACT_SNAKE_BETA;
+    constexpr int H = Acc<V>::H;
     ptx::grid_dep_wait();
-    const Place p = place<V>(a);
+    const Place p = place<V>(a, gridDim.x - 1 - blockIdx.x);
     if (!p.live) return;
     const int n = valid_rows(a, p.b);
     const int r0 = min(p.ch * a.rows, a.T), r1 = min(r0 + a.rows, a.T);
-    float mu[V], sc[V], bi[V], al[V], ib[V];
-    load_param<V>(a.weight, p.c, a.C, 1.f, sc);
-    load_param<V>(a.bias, p.c, a.C, 0.f, bi);
-    if (ACT == MH3A_ACT_SNAKE_BETA) {
-        load_param<V>(a.alpha, p.c, a.C, 0.f, al);
-        load_param<V>(a.beta, p.c, a.C, 0.f, ib);
-    }
+    float mu[2 * H], sc[2 * H], bi[2 * H], al[2 * H], ib[2 * H];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int g = p.b * a.G + min(p.c + i, a.C - 1) / a.D;
-        mu[i] = a.mean[g];
-        sc[i] *= a.rstd[g];
-        if (ACT == MH3A_ACT_SNAKE_BETA) ib[i] = 1.0f / (ib[i] + 1e-9f);
+    for (int i = 0; i < 2 * H; ++i) {
+        const int c = min(p.c + i, a.C - 1), g = p.b * a.G + c / a.D;
+        mu[i] = -a.mean[g];
+        sc[i] = a.rstd[g] * (a.weight ? __ldg(a.weight + c) : 1.f);
+        bi[i] = a.bias ? __ldg(a.bias + c) : 0.f;
+        al[i] = kSnake ? __ldg(a.alpha + c) : 0.f;
+        ib[i] = kSnake ? rcp_ftz(__ldg(a.beta + c) + 1e-9f) : 0.f;
     }
-    const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c;
-    T* y = static_cast<T*>(a.out) + (long long)p.b * a.T * a.C + p.c;
+    const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c + (long long)(r0 + p.ty) * a.xr;
+    T* y = static_cast<T*>(a.out) + ((long long)p.b * a.T + r0 + p.ty) * a.C + p.c;
+    const long long xs = (long long)p.TY * a.xr, ys = (long long)p.TY * a.C;
+    const int top = min(n, r1) - r0;
+    const int mine = top > p.ty ? (top - p.ty + p.TY - 1) / p.TY : 0;
+    auto put = [&](const Pack<T, V>& in, T* to) {
+        Acc<V> f;
+        unpack_acc<T, V>(in, f);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float2 u = __ffma2_rn(__fadd2_rn(f.v[i], make_float2(mu[2 * i], mu[2 * i + 1])), make_float2(sc[2 * i], sc[2 * i + 1]),
+                                        make_float2(bi[2 * i], bi[2 * i + 1]));
+            f.v[i] = act_fwd2<ACT, kPrecise>(u, make_float2(al[2 * i], al[2 * i + 1]), make_float2(ib[2 * i], ib[2 * i + 1]));
+        }
+        if constexpr (V == 1) *to = from_f<T>(f.v[0].x);
+        else store_pairs<T, V>(to, f.v);
+    };
     constexpr int U = 4;
-    for (int t = r0 + p.ty; t < r1; t += U * p.TY) {
+    int k = 0;
+    for (; k + U <= mine; k += U) {
         Pack<T, V> in[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int row = t + k * p.TY;
-            if (row < r1 && row < n) in[k] = load_pack<T, V>(x + (long long)row * a.xr);
-        }
+        for (int j = 0; j < U; ++j) in[j] = load_pack<T, V>(x + j * xs);
+        x += U * xs;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int row = t + k * p.TY;
-            if (row >= r1) break;
-            float f[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                f[i] = row < n ? act_fwd<ACT, kPrecise>(fmaf(to_f<T>(in[k].v[i]) - mu[i], sc[i], bi[i]),
-                                                        ACT == MH3A_ACT_SNAKE_BETA ? al[i] : 0.f,
-                                                        ACT == MH3A_ACT_SNAKE_BETA ? ib[i] : 0.f)
-                               : 0.f;
-            store_pack<T, V>(y + (long long)row * a.C, f);
-        }
+        for (int j = 0; j < U; ++j) put(in[j], y + j * ys);
+        y += U * ys;
     }
+    for (; k < mine; ++k, x += xs, y += ys) put(load_pack<T, V>(x), y);
+    const Pack<T, V> zero{};
+    for (; p.ty + k * p.TY < r1 - r0; ++k, y += ys) *reinterpret_cast<Pack<T, V>*>(y) = zero;
 }
 
 // --------------------------------------------------------------------------------- backward
@@ -247,7 +287,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_partial(const NormArgs a)
     constexpr bool kPrecise = sizeof(T) == 4;
     constexpr int NS = kSums<ACT>;
     ptx::grid_dep_wait();
-    const Place p = place<V>(a);
+    const Place p = place<V>(a, blockIdx.x);
     const int n = valid_rows(a, p.b);
     const int r0 = min(p.ch * a.rows, n), r1 = min(r0 + a.rows, n);
     float acc[V][NS];
@@ -397,7 +437,7 @@ template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(const NormArgs a, const float2* means) {
     constexpr bool kPrecise = sizeof(T) == 4;
     ptx::grid_dep_wait();
-    const Place p = place<V>(a);
+    const Place p = place<V>(a, blockIdx.x);
     if (!p.live) return;
     const int n = valid_rows(a, p.b);
     const int r0 = min(p.ch * a.rows, a.T), r1 = min(r0 + a.rows, a.T);
@@ -483,50 +523,48 @@ bool go(F kern, long long grid, int threads, cudaStream_t s, Args... args) {
 
 // Shared memory of a resident block: two blocks an SM where the slab allows, else one.
 constexpr int kResTwo = 112 * 1024, kResOne = 224 * 1024;
+static const long long kResMax = (getenv("RMAX") ? atoi(getenv("RMAX")) : 16) * 1000000LL;
+
+FastDiv fast_div(unsigned d) { return FastDiv{d, (unsigned)(((1ull << 32) + d - 1) / d)}; }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-// Divides a tensor for the resident form; false where one cluster cannot hold an item's slab.
-// Slabs are whole groups and whole vectors.  `bytes_row` are kept per channel and row (x, or x and
-// dy), `extra(nt, W)` beside them.
+// Divides a tensor for the resident form; false where it does not serve.  Slabs are whole groups and
+// whole vectors.  `bytes_row` are kept per channel and row (x, or x and dy), `extra(W, S)` beside.
 template <typename Extra>
-bool plan_resident(const NormArgs& a, int V, int e, int bytes_row, Extra extra, Resident* r, int* threads) {
-    const int unit = a.D / gcd(a.D, V) * V;
-    const int units = a.C / unit;
-    for (int want : {128, 64, 32}) {
-        int k = 1;
-        while (k < units && (units % k || k * unit * e < want)) ++k;
-        const int W = k * unit;
-        const int slabs = a.C / W;
-        // more blocks than this leave SMs idle no longer
-        if (want == 128 && k > 1 && (long long)a.B * slabs * 8 < 2 * kSms && a.T >= 128) continue;
-        for (int limit : {kResTwo, kResOne}) {
-            for (int nt : {256, 512}) {
-                if (W / V > nt) continue;
-                auto bytes = [&](int s) { return (long long)((a.T + s - 1) / s) * W * bytes_row + extra(nt, W); };
-                int S = 1;
-                while (S < 16 && bytes(S) > limit) S *= 2;
-                if (bytes(S) > limit) continue;
-                while (S < 8 && (long long)a.B * slabs * S * 2 <= 2 * kSms && (a.T + 2 * S - 1) / (2 * S) >= 16) S *= 2;
-                const int rows = (a.T + S - 1) / S;
-                // 512 threads once a thread of 256 would have more than 16 rows
-                if (nt == 256 && (long long)rows * (W / V) > 16 * 256 && W / V <= 512) continue;
-                *r = Resident{S, rows, W, slabs, (int)bytes(S)};
-                *threads = nt;
-                return true;
-            }
+bool plan_resident(const NormArgs& a, int V, int e, int bytes_row, Extra extra, Resident* r) {
+    const long long unit_l = (long long)a.D / gcd(a.D, V) * V;
+    if (unit_l > kResThreads * V || a.B > 65535 || (long long)a.B * a.T * a.C * bytes_row > kResMax) return false;
+    const int unit = (int)unit_l, units = a.C / unit;
+    for (int limit : {kResTwo, kResOne}) {
+        for (int want : {128, 64}) {
+            int k = 1;
+            while (k < units && (units % k || k * unit * e < want)) ++k;
+            const int W = k * unit;
+            const int slabs = a.C / W;
+            if (slabs > 65535 || W / V > kResThreads) continue;
+            // narrower slabs while whole clusters of wide ones would leave SMs idle
+            if (want == 128 && k > 1 && (long long)a.B * slabs * 8 < 2 * kSms && a.T >= 128) continue;
+            auto bytes = [&](int s) { return (long long)((a.T + s - 1) / s) * W * bytes_row + extra(W, s); };
+            int S = 1;
+            while (S < 16 && bytes(S) > limit) S *= 2;
+            if (bytes(S) > limit) continue;
+            while (S < 8 && (long long)a.B * slabs * S * 2 <= 2 * kSms && (a.T + 2 * S - 1) / (2 * S) >= 16) S *= 2;
+            *r = Resident{S, (a.T + S - 1) / S, W, slabs, (int)bytes(S), fast_div(kResThreads / (W / V)),
+                          fast_div(W / V), fast_div(a.D), fast_div(a.D % V ? a.D : a.D / V)};
+            return true;
         }
     }
     return false;
 }
 
 template <typename K, typename... Args>
-bool go_resident(K kern, const NormArgs& a, const Resident& r, int threads, cudaStream_t s, Args... args) {
+bool go_resident(K kern, const NormArgs& a, const Resident& r, cudaStream_t s, Args... args) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kResOne) != cudaSuccess) return false;
     if (r.S > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((long long)a.B * r.slabs * r.S));
-    cfg.blockDim = dim3(threads);
+    cfg.gridDim = dim3(r.S, r.slabs, a.B);
+    cfg.blockDim = dim3(kResThreads);
     cfg.dynamicSmemBytes = r.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -540,15 +578,10 @@ bool go_resident(K kern, const NormArgs& a, const Resident& r, int threads, cuda
     return cudaLaunchKernelEx(&cfg, kern, a, r, args...) == cudaSuccess;
 }
 
-template <typename T, int V, int ACT, int NT>
-bool forward_resident(const NormArgs& a, const Resident& r, cudaStream_t s) {
-    return a.D % V == 0 ? go_resident(k_norm_resident<T, V, ACT, true, NT>, a, r, NT, s)
-                        : go_resident(k_norm_resident<T, V, ACT, false, NT>, a, r, NT, s);
-}
-
 template <typename T, int V, int ACT>
-bool forward_resident(const NormArgs& a, const Resident& r, int threads, cudaStream_t s) {
-    return threads == 256 ? forward_resident<T, V, ACT, 256>(a, r, s) : forward_resident<T, V, ACT, 512>(a, r, s);
+bool forward_resident(const NormArgs& a, const Resident& r, cudaStream_t s) {
+    return a.D % V == 0 ? go_resident(k_norm_resident<T, V, ACT, true>, a, r, s)
+                        : go_resident(k_norm_resident<T, V, ACT, false>, a, r, s);
 }
 
 template <typename T, int V>
@@ -567,13 +600,12 @@ template <typename T>
 bool forward(NormArgs& a, int act, bool vec, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
     Resident r;
-    int nt;
-    auto extra = [&](int threads, int W) { return res_fwd_extra(threads, W, a.D, V); };
-    if (vec && plan_resident(a, V, sizeof(T), sizeof(T), extra, &r, &nt)) {
+    auto extra = [&](int W, int S) { return res_fwd_extra(W, a.D, V, S); };
+    if (vec && plan_resident(a, V, sizeof(T), sizeof(T), extra, &r)) {
         switch (act) {
-            case MH3A_ACT_SILU: return forward_resident<T, V, MH3A_ACT_SILU>(a, r, nt, s);
-            case MH3A_ACT_SNAKE_BETA: return forward_resident<T, V, MH3A_ACT_SNAKE_BETA>(a, r, nt, s);
-            default: return forward_resident<T, V, MH3A_ACT_NONE>(a, r, nt, s);
+            case MH3A_ACT_SILU: return forward_resident<T, V, MH3A_ACT_SILU>(a, r, s);
+            case MH3A_ACT_SNAKE_BETA: return forward_resident<T, V, MH3A_ACT_SNAKE_BETA>(a, r, s);
+            default: return forward_resident<T, V, MH3A_ACT_NONE>(a, r, s);
         }
     }
     plan_general(&a, vec ? V : 1);
@@ -648,6 +680,11 @@ size_t general_bytes(const mh3a_norm* p, int backward) {
     return (most + 255) / 256 * 256;
 }
 
+// Whether whole vectors can be used: parameters are then read by 16-byte loads.
+bool params_fit(const NormArgs& a) {
+    return aligned(a.weight, 16) && aligned(a.bias, 16) && aligned(a.alpha, 16) && aligned(a.beta, 16);
+}
+
 bool strides_fit(long long b, long long r, int V) { return b % V == 0 && r % V == 0; }
 
 }  // namespace norm
@@ -677,7 +714,7 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const vo
     a.mean = mean;
     a.rstd = rstd;
     a.ws = static_cast<float*>(workspace);
-    const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(y, 16) && strides_fit(a.xb, a.xr, V);
+    const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(y, 16) && strides_fit(a.xb, a.xr, V) && params_fit(a);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     bool ok;
     switch (p->dtype) {
@@ -718,7 +755,7 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p,
     a.dbeta = dbeta;
     a.ws = static_cast<float*>(workspace);
     const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(dx, 16) &&
-                     strides_fit(a.xb, a.xr, V) && strides_fit(a.gb, a.gr, V);
+                     strides_fit(a.xb, a.xr, V) && strides_fit(a.gb, a.gr, V) && params_fit(a);
     plan_general(&a, vec ? V : 1);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     bool ok;

@@ -3,18 +3,21 @@
 // A cluster of S blocks owns one item's slab of channels (whole groups, at least 64 bytes of a row
 // where the tensor has them); each block keeps a chunk of the slab's rows in shared memory, so the
 // statistics and the elementwise pass read global memory once and write it once.  The S blocks
-// exchange their partial sums through distributed shared memory.  A thread reads back only what it
+// exchange their partial sums through distributed shared memory: each block stores its own into every
+// peer's inbox with st.async, which counts the bytes on the peer's mbarrier.  A cluster barrier in
+// its place would wait for the block's outstanding output stores (measured: 202 us against XXX at
+// the batch of sixteen 20 s items, 256 channels, bf16).  A thread reads back only what it
 // copied itself (its channels are fixed, its rows are every TY-th), so no barrier stands between the
 // copies and their use, and the statistics of the rows that have arrived are formed while the later
 // ones are on their way.
 #pragma once
 
-#include <cooperative_groups.h>
-
 #include "norm_kernels.cuh"
 
 namespace mh3a {
 namespace norm {
+
+constexpr int kResThreads = 256;
 
 // How a resident launch divides the tensor.
 struct Resident {
@@ -23,6 +26,10 @@ struct Resident {
     int W;      // channels per slab
     int slabs;  // slabs per row
     int smem;   // dynamic shared memory, bytes
+    FastDiv ty;    // rows of threads
+    FastDiv w;     // vectors per slab row
+    FastDiv D;     // channels per group
+    FastDiv span;  // partial sums per group and row of threads
 };
 
 struct ResPlace {
@@ -30,22 +37,24 @@ struct ResPlace {
     bool live;
 };
 
-template <int V, int NT>
+template <int V>
 __device__ __forceinline__ ResPlace res_place(const Resident& r) {
     ResPlace p;
-    p.rank = blockIdx.x % r.S;
-    const unsigned unit = blockIdx.x / r.S;
-    p.c0 = (int)(unit % r.slabs) * r.W;
-    p.b = unit / r.slabs;
-    p.w = r.W / V;
-    p.tx = threadIdx.x % p.w;
-    p.ty = threadIdx.x / p.w;
-    p.TY = NT / p.w;
+    p.rank = blockIdx.x;
+    p.c0 = blockIdx.y * r.W;
+    p.w = r.w.d;
+    p.ty = threadIdx.x / r.w;
+    p.tx = threadIdx.x - p.ty * p.w;
+    p.TY = r.ty.d;
+    p.b = blockIdx.z;
     p.live = p.ty < p.TY;
     p.c = p.c0 + p.tx * V;
     return p;
 }
 
+__device__ __forceinline__ void cp_async16_to(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -59,10 +68,24 @@ struct alignas(16) Part {
 };
 
 // Shared memory behind the data: one Part per thread (and channel, where vectors straddle groups),
-// then per group the block's Part and the final (mean, rstd).
-__host__ __device__ constexpr int res_fwd_extra(int nt, int W, int D, int V) {
-    return nt * (D % V ? V : 1) * 16 + (W / D) * 24;
+// an inbox of one Part per peer and group with its mbarrier, and the final (mean, rstd).
+__host__ __device__ constexpr int res_fwd_extra(int W, int D, int V, int S) {
+    return kResThreads * (D % V ? V : 1) * 16 + (W / D) * (16 * S + 8) + 16;
 }
+
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, int rank) {
+    uint32_t to;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(addr), "r"(rank));
+    return to;
+}
+// 16 bytes into a peer's shared memory, counted on the peer's mbarrier.
+__device__ __forceinline__ void send16(uint32_t to, uint32_t bar, float4 v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
@@ -73,12 +96,13 @@ __device__ __forceinline__ F warp_sum(F v) {
 
 // The block's statistics of one group (the result is in all lanes of the warp): entries (row of
 // threads, first .. first + span) of `part`, a few per lane, put together in fp64.
-__device__ __forceinline__ Part group_stats(const Part* part, int ty_n, int width, int first, int span) {
-    const int lane = threadIdx.x & 31, m = ty_n * span;
+__device__ __forceinline__ Part group_stats(const Part* part, int ty_n, int width, int first, FastDiv span) {
+    const int lane = threadIdx.x & 31, m = ty_n * span.d;
     float n = 0.f;
     double s = 0.0;
     for (int i = lane; i < m; i += 32) {
-        const Part v = part[(i / span) * width + first + i % span];
+        const int row = (unsigned)i / span;
+        const Part v = part[row * (width - (int)span.d) + first + i];
         n += v.n;
         if (v.n > 0.f) s += ((double)v.hi + (double)v.lo) * v.n;
     }
@@ -86,7 +110,8 @@ __device__ __forceinline__ Part group_stats(const Part* part, int ty_n, int widt
     const double mean = n > 0.f ? warp_sum(s) / n : 0.0;
     double q = 0.0;
     for (int i = lane; i < m; i += 32) {
-        const Part v = part[(i / span) * width + first + i % span];
+        const int row = (unsigned)i / span;
+        const Part v = part[row * (width - (int)span.d) + first + i];
         const double d = (double)v.hi + (double)v.lo - mean;
         if (v.n > 0.f) q += fma(v.n * d, d, (double)v.m2);
     }
@@ -95,124 +120,129 @@ __device__ __forceinline__ Part group_stats(const Part* part, int ty_n, int widt
 }
 
 // WHOLE: no vector straddles two groups (D is a multiple of V).
-template <typename T, int V, int ACT, bool WHOLE, int NT>
-__global__ void __launch_bounds__(NT) k_norm_resident(const NormArgs a, const Resident r) {
+template <typename T, int V, int ACT, bool WHOLE>
+__global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a, const Resident r) {
     constexpr bool kPrecise = sizeof(T) == 4;
     constexpr int H = V / 2;
     constexpr int P = WHOLE ? 1 : H;  // pairs of partial sums a thread keeps
-    namespace cg = cooperative_groups;
+    constexpr bool kSnake = ACT == MH3A_ACT_SNAKE_BETA;
     extern __shared__ __align__(16) unsigned char smem[];
+    const ResPlace p = res_place<V>(r);
+    const int r0 = min(p.rank * r.rows, a.T), r1 = min(r0 + r.rows, a.T);
+    Part* part = reinterpret_cast<Part*>(smem + (size_t)r.rows * r.W * sizeof(T));
+    Part* inbox = part + kResThreads * (WHOLE ? 1 : V);  // [S][ng]
+    const int ng = (unsigned)r.W / r.D;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(inbox + r.S * ng);
+    float2* fin = reinterpret_cast<float2*>(bar + 2);  // (mean, rstd)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int next = p.TY * p.w;  // between a thread's rows in shared memory, in vectors
+    const int width = WHOLE ? p.w : r.W;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(bar, 1);
+        ptx::fence_mbar_init();
+        ptx::mbar_arrive_expect_tx(bar, r.S * ng * 16);
+    }
+    cluster_arrive();
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    const ResPlace p = res_place<V, NT>(r);
     const int n = valid_rows(a, p.b);
-    const int r0 = min(p.rank * r.rows, a.T), r1 = min(r0 + r.rows, a.T);
     const int have = max(0, min(n, r1) - r0);  // valid rows of this chunk
-    Pack<T, V>* data = reinterpret_cast<Pack<T, V>*>(smem) + p.tx;
-    Part* part = reinterpret_cast<Part*>(smem + (size_t)r.rows * r.W * sizeof(T));
-    Part* loc = part + NT * (WHOLE ? 1 : V);
-    const int ng = r.W / a.D;
-    float2* fin = reinterpret_cast<float2*>(loc + ng);  // (mean, rstd)
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    // rows of this thread: ty + TY k, k < mine; `per` of them in each copy group
-    const int mine = p.live ? (have - p.ty + p.TY - 1) / p.TY : 0;
+    // this thread's rows: ty + TY k, k < mine; `per` of them in each copy group
+    const int mine = p.live && have > p.ty ? (int)((unsigned)(have - p.ty + p.TY - 1) / r.ty) : 0;
     const int per = (mine + kParts - 1) / kParts;
     {
         const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c + (long long)(r0 + p.ty) * a.xr;
         const long long step = (long long)p.TY * a.xr;
+        uint32_t to = ptx::smem_u32(smem) + (p.tx + p.ty * p.w) * 16;
         int k = 0;
 #pragma unroll
         for (int g = 0; g < kParts; ++g) {
-            for (int e = min(mine, (g + 1) * per); k < e; ++k, x += step) ptx::cp_async16(data + (p.ty + k * p.TY) * p.w, x);
+#pragma unroll 4
+            for (int e = min(mine, (g + 1) * per); k < e; ++k, x += step, to += next * 16) cp_async16_to(to, x);
             ptx::cp_async_commit();
         }
     }
     // what does not depend on the rows, while they arrive
-    const double inv_count = n > 0 ? 1.0 / ((double)n * a.D) : 0.0;
-    float2 sc[H], bi[H], al[H], ib[H];
+    float2 w[H], bi[H], al[H], ib[H];
     if (p.live) {
-        load_param<V>(a.weight, p.c, a.C, 1.f, reinterpret_cast<float(&)[V]>(sc));
-        load_param<V>(a.bias, p.c, a.C, 0.f, reinterpret_cast<float(&)[V]>(bi));
-        if (ACT == MH3A_ACT_SNAKE_BETA) {
-            load_param<V>(a.alpha, p.c, a.C, 0.f, reinterpret_cast<float(&)[V]>(al));
-            load_param<V>(a.beta, p.c, a.C, 0.f, reinterpret_cast<float(&)[V]>(ib));
+        load_param_vec<V>(a.weight, p.c, 1.f, w);
+        load_param_vec<V>(a.bias, p.c, 0.f, bi);
+        if (kSnake) {
+            load_param_vec<V>(a.alpha, p.c, 0.f, al);
+            load_param_vec<V>(a.beta, p.c, 0.f, ib);
 #pragma unroll
-            for (int i = 0; i < H; ++i) ib[i] = make_float2(1.0f / (ib[i].x + 1e-9f), 1.0f / (ib[i].y + 1e-9f));
+            for (int i = 0; i < H; ++i) ib[i] = make_float2(rcp_ftz(ib[i].x + 1e-9f), rcp_ftz(ib[i].y + 1e-9f));
         }
     }
+    const Pack<T, V>* mydata = reinterpret_cast<const Pack<T, V>*>(smem) + p.tx + p.ty * p.w;
 
-    // Sums of deviations from a value near the thread's mean: the mean of its first rows.  An outlier
-    // among them moves it by a fraction only, so the squares cancel by a factor of rows / 16 at worst.
+    // Sums of deviations from a value near the thread's mean: the mean of its first rows.  An
+    // outlier among them moves it by a fraction only, so the squares cancel by a factor of
+    // rows / 16 at worst.
     float2 sh[P], s[P], q[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) sh[i] = s[i] = q[i] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int g = 0; g < kParts; ++g) {
-        if (g == 0) cp_async_wait_group<3>();
-        if (g == 1) cp_async_wait_group<2>();
-        if (g == 2) cp_async_wait_group<1>();
-        if (g == 3) cp_async_wait_group<0>();
+        if (g == 0) cp_async_wait_group<kParts - 1>();
+        if (g == 1) cp_async_wait_group<kParts - 2>();
+        if (g == 2) cp_async_wait_group<kParts - 3>();
+        if (g == 3) cp_async_wait_group<kParts - 4>();
         if (g == 0 && mine > 0) {
             const int m = min(per, 4);
             for (int k = 0; k < m; ++k) {
                 float2 f[H];
-                unpack_pairs<T, V>(data[(p.ty + k * p.TY) * p.w], f);
+                unpack_pairs<T, V>(mydata[k * next], f);
 #pragma unroll
                 for (int i = 0; i < H; ++i) sh[WHOLE ? 0 : i] = __fadd2_rn(sh[WHOLE ? 0 : i], f[i]);
             }
-            if (WHOLE) {
-                const float v = -(sh[0].x + sh[0].y) / (float)(m * V);
-                sh[0] = make_float2(v, v);
-            } else {
-                const float v = -1.0f / (float)m;
+            const float im = -rcp_ftz((float)(WHOLE ? m * V : m));
+            if (WHOLE) sh[0].x = sh[0].y = sh[0].x + sh[0].y;
 #pragma unroll
-                for (int i = 0; i < P; ++i) sh[i] = __fmul2_rn(sh[i], make_float2(v, v));
-            }
+            for (int i = 0; i < P; ++i) sh[i] = __fmul2_rn(sh[i], make_float2(im, im));
         }
-        for (int k = g * per, e = min(mine, (g + 1) * per); k < e; ++k) {
+        const Pack<T, V>* at = mydata + g * per * next;
+#pragma unroll 2
+        for (int k = min(mine, (g + 1) * per) - g * per; k > 0; --k, at += next) {
             float2 f[H];
-            unpack_pairs<T, V>(data[(p.ty + k * p.TY) * p.w], f);
+            unpack_pairs<T, V>(*at, f);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                constexpr int Z = 0;
-                const int j = WHOLE ? Z : i;
+                const int j = WHOLE ? 0 : i;
                 const float2 d = __fadd2_rn(f[i], sh[j]);
                 s[j] = __fadd2_rn(s[j], d);
                 q[j] = __ffma2_rn(d, d, q[j]);
             }
         }
     }
-    const int width = WHOLE ? p.w : r.W;
     if (p.live) {
+        const float cnt = (float)(WHOLE ? mine * V : mine), ic = mine > 0 ? rcp_ftz(cnt) : 0.f;
         if (WHOLE) {
-            const float cnt = (float)mine * V, sum = s[0].x + s[0].y;
-            const float lo = mine > 0 ? sum / cnt : 0.f;
+            const float sum = s[0].x + s[0].y, lo = sum * ic;
             part[p.ty * width + p.tx] = Part{-sh[0].x, lo, q[0].x + q[0].y - sum * lo, cnt};
         } else {
-            const float cnt = (float)mine, ic = mine > 0 ? 1.0f / cnt : 0.f;
+            Part* to = part + p.ty * width + p.tx * V;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                part[p.ty * width + p.tx * V + 2 * i] = Part{-sh[i].x, s[i].x * ic, q[i].x - s[i].x * s[i].x * ic, cnt};
-                part[p.ty * width + p.tx * V + 2 * i + 1] = Part{-sh[i].y, s[i].y * ic, q[i].y - s[i].y * s[i].y * ic, cnt};
+                to[2 * i] = Part{-sh[i].x, s[i].x * ic, q[i].x - s[i].x * s[i].x * ic, cnt};
+                to[2 * i + 1] = Part{-sh[i].y, s[i].y * ic, q[i].y - s[i].y * s[i].y * ic, cnt};
             }
         }
     }
     __syncthreads();
-    const int span = WHOLE ? a.D / V : a.D;  // entries per group and row of threads
-    for (int g = warp; g < ng; g += NT / 32) {
-        const Part v = group_stats(part, p.TY, width, g * span, span);
-        if (lane == 0) loc[g] = v;
+    cluster_wait();  // the peers' mbarriers are initialised
+    for (int g = warp; g < ng; g += kResThreads / 32) {
+        const Part o = group_stats(part, p.TY, width, g * r.span.d, r.span);
+        if (lane < r.S)
+            send16(peer_smem(ptx::smem_u32(inbox + p.rank * ng + g), lane), peer_smem(ptx::smem_u32(bar), lane),
+                   make_float4(o.hi, o.lo, o.m2, o.n));
     }
-    if (r.S > 1) cg::this_cluster().sync();
-    else __syncthreads();
-    for (int g = warp; g < ng; g += NT / 32) {
+    const bool arrived = ptx::mbar_wait(bar, 0);  // so no peer sends to this block after it has ended
+    for (int g = warp; g < ng; g += kResThreads / 32) {
         Part o{0.f, 0.f, 0.f, 0.f};
-        if (r.S > 1) {
-            if (lane < r.S) o = *cg::this_cluster().map_shared_rank(loc + g, lane);
-        } else if (lane == 0) {
-            o = loc[g];
-        }
+        if (lane < r.S) o = inbox[lane * ng + g];
+        if (!arrived) o.m2 = __int_as_float(0x7fffffff);  // never expected: NaN rather than stale sums
+        const double inv_count = n > 0 ? 1.0 / ((double)n * a.D) : 0.0;
         const double m = (double)o.hi + (double)o.lo;
         double sum = o.n > 0.f ? m * o.n : 0.0;
 #pragma unroll
@@ -232,37 +262,33 @@ __global__ void __launch_bounds__(NT) k_norm_resident(const NormArgs a, const Re
         }
     }
     __syncthreads();
-    if (r.S > 1) cg::this_cluster().barrier_arrive();
 
     if (p.live) {
-        float2 mu[H];
+        float2 mu[H], sc[H];
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            const float2 f = fin[(p.tx * V + 2 * i) / a.D], h = WHOLE ? f : fin[(p.tx * V + 2 * i + 1) / a.D];
+            const float2 f = fin[(unsigned)(p.tx * V + (WHOLE ? 0 : 2 * i)) / r.D];
+            const float2 h = WHOLE ? f : fin[(unsigned)(p.tx * V + 2 * i + 1) / r.D];
             mu[i] = make_float2(-f.x, -h.x);
-            sc[i] = __fmul2_rn(sc[i], make_float2(f.y, h.y));
+            sc[i] = __fmul2_rn(w[i], make_float2(f.y, h.y));
         }
-        T* y = static_cast<T*>(a.out) + ((long long)p.b * a.T + r0) * a.C + p.c;
-        for (int t = p.ty; t < r1 - r0; t += p.TY) {
-            float f[V];
-            if (t < have) {
-                float2 f2[H];
-                unpack_pairs<T, V>(data[t * p.w], f2);
+        T* y = static_cast<T*>(a.out) + ((long long)p.b * a.T + r0 + p.ty) * a.C + p.c;
+        const long long step = (long long)p.TY * a.C;
+        const Pack<T, V>* at = mydata;
+#pragma unroll 2
+        for (int k = 0; k < mine; ++k, at += next, y += step) {
+            float2 f[H];
+            unpack_pairs<T, V>(*at, f);
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    const float2 u = __ffma2_rn(__fadd2_rn(f2[i], mu[i]), sc[i], bi[i]);
-                    constexpr bool kSnake = ACT == MH3A_ACT_SNAKE_BETA;
-                    f[2 * i] = act_fwd<ACT, kPrecise>(u.x, kSnake ? al[i].x : 0.f, kSnake ? ib[i].x : 0.f);
-                    f[2 * i + 1] = act_fwd<ACT, kPrecise>(u.y, kSnake ? al[i].y : 0.f, kSnake ? ib[i].y : 0.f);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) f[i] = 0.f;
+            for (int i = 0; i < H; ++i) {
+                const float2 u = __ffma2_rn(__fadd2_rn(f[i], mu[i]), sc[i], bi[i]);
+                f[i] = act_fwd2<ACT, kPrecise>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u);
             }
-            store_pack<T, V>(y + (long long)t * a.C, f);
+            store_pairs<T, V>(y, f);
         }
+        const Pack<T, V> zero{};  // rows behind the item's length
+        for (int k = mine; p.ty + k * p.TY < r1 - r0; ++k, y += step) *reinterpret_cast<Pack<T, V>*>(y) = zero;
     }
-    if (r.S > 1) cg::this_cluster().barrier_wait();  // peers may still read this block's sums
 }
 
 }  // namespace norm
