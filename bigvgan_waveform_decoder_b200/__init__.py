@@ -14,5 +14,6 @@ def __getattr__(name):
     if name in ("group_norm_act", "group_norm_act_backward"):
         from . import ops
 
-        return getattr(ops, name)
+        globals()[name] = getattr(ops, name)
+        return globals()[name]
     raise AttributeError(name)

@@ -243,5 +243,34 @@ __device__ __forceinline__ float act_slope(float u, float al, float ib, float* p
     return 1.0f;
 }
 
+// The same for a pair.
+template <int ACT, bool PRECISE>
+__device__ __forceinline__ float2 act_slope2(float2 u, float2 al, float2 ib, float2* pa, float2* pb) {
+    if (PRECISE || ACT == MH3A_ACT_NONE) {
+        float2 s;
+        s.x = act_slope<ACT, PRECISE>(u.x, al.x, ib.x, &pa->x, &pb->x);
+        s.y = act_slope<ACT, PRECISE>(u.y, al.y, ib.y, &pa->y, &pb->y);
+        return s;
+    }
+    const float2 one = make_float2(1.f, 1.f);
+    if (ACT == MH3A_ACT_SILU) {
+        const float2 t = __fmul2_rn(u, make_float2(-1.44269504088896341f, -1.44269504088896341f));
+        const float2 e = __fadd2_rn(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), one);
+        const float2 s = make_float2(rcp_ftz(e.x), rcp_ftz(e.y));
+        return __fmul2_rn(s, __ffma2_rn(u, __ffma2_rn(s, make_float2(-1.f, -1.f), one), one));
+    }
+    const float2 v = __fmul2_rn(al, u);
+    const float2 sn = make_float2(__sinf(v.x), __sinf(v.y)), cs = make_float2(__cosf(v.x), __cosf(v.y));
+    const float2 s2 = __fmul2_rn(__fmul2_rn(__fadd2_rn(sn, sn), cs), ib);
+    *pa = __fmul2_rn(u, s2);
+    *pb = __fmul2_rn(sn, sn);
+    return __ffma2_rn(al, s2, one);
+}
+
+// Sums of one channel in the backward pass: 0 du, 1 du xh, 2 dy * (factor of dalpha), 3 dy * (factor
+// of dbeta).
+template <int ACT>
+constexpr int kSums = ACT == MH3A_ACT_SNAKE_BETA ? 4 : 2;
+
 }  // namespace norm
 }  // namespace mh3a

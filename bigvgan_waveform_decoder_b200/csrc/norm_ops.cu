@@ -5,11 +5,13 @@
 //
 // Both directions are bound by memory: a handful of operations an element against 4 to 12 bytes.
 //
-// The general form takes any size, in passes over global memory: per-channel partial sums of a
-// chunk of rows, their combination in fixed order, then the elementwise pass.  Rows are channels
-// wide, so a warp reads whole rows (512 bytes) and every thread keeps one fixed run of V channels:
-// its statistics stay per channel in registers, and groups of any width, also ones that end inside
-// a vector, are put together only at the end.
+// Tensors up to 100 MB take the resident form (norm_resident.cuh), one pass over global memory.
+//
+// The general form takes any size and alignment, in passes over global memory: per-channel partial
+// sums of a chunk of rows, their combination in fixed order, then the elementwise pass.  Rows are
+// channels wide, so a warp reads whole rows (512 bytes) and every thread keeps one fixed run of V
+// channels: its statistics stay per channel in registers, and groups of any width, also ones that end
+// inside a vector, are put together only at the end.
 #include <algorithm>
 
 #include "norm_kernels.cuh"
@@ -20,7 +22,7 @@ namespace mh3a {
 namespace norm {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 8;  // rows a thread has in flight
+constexpr int kBatch = 4;  // rows a thread has in flight
 
 // One block's place: item b, channel tile, row chunk.
 struct Place {
@@ -74,10 +76,10 @@ __device__ __forceinline__ void unpack_acc(const Pack<T, V>& p, Acc<V>& f) {
 }
 
 // Per-channel statistics of one chunk of rows.  A thread adds up deviations from the mean of its
-// first 8 rows, so neither a large offset nor an outlier (which moves that mean by an eighth) costs
+// first rows, so neither a large offset nor an outlier (which moves that mean by a quarter) costs
 // accuracy; threads, warps and chunks are merged as (mean, squared deviations).
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) k_norm_partial(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) k_norm_partial(const NormArgs a) {
     constexpr int H = Acc<V>::H;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
@@ -179,6 +181,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_partial(const NormArgs a) {
     }
 }
 
+constexpr int kStatThreads = 512;
+
 __device__ __forceinline__ double block_sum(double v, double* sh) {
 #pragma unroll
     for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -186,47 +190,52 @@ __device__ __forceinline__ double block_sum(double v, double* sh) {
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
     __syncthreads();
     double s = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += sh[w];
+#pragma unroll
+    for (int w = 0; w < kStatThreads / 32; ++w) s += sh[w];
     return s;
 }
 
-// mean and rstd of one (item, group) from the chunks' statistics, in fp64.
-__global__ void __launch_bounds__(kThreads) k_norm_stats(const NormArgs a) {
+// mean and rstd of one (item, group) from the chunks' statistics, in fp64.  `tx` threads (a power of
+// two) stand along the group's channels, the others along the chunks.
+__global__ void __launch_bounds__(kStatThreads) k_norm_stats(const NormArgs a, int tx) {
     ptx::grid_dep_wait();
-    __shared__ double sh[kThreads / 32];
+    ptx::grid_dep_launch();
+    __shared__ double sh[kStatThreads / 32];
     const int b = blockIdx.x / a.G, g = blockIdx.x % a.G;
     const int n = valid_rows(a, b);
     const float4* part = reinterpret_cast<const float4*>(a.ws) + (long long)b * a.chunks * a.C + (long long)g * a.D;
-    const int used = a.rows > 0 ? (n + a.rows - 1) / a.rows : 0;
-    const long long m = (long long)used * a.D;
+    const int used = (n + a.rows - 1) / a.rows;
+    const int lx = threadIdx.x & (tx - 1), ly = threadIdx.x / tx, ny = kStatThreads / tx;
     double s = 0;
-    for (long long i = threadIdx.x; i < m; i += kThreads) {
-        const int ch = (int)(i / a.D), c = (int)(i % a.D);
-        const int rows = min(a.rows, n - ch * a.rows);
-        const float4 v = part[(long long)ch * a.C + c];
-        s += ((double)v.x + (double)v.y) * rows;
+    for (int c = lx; c < a.D; c += tx) {
+#pragma unroll 4
+        for (int ch = ly; ch < used; ch += ny) {
+            const float4 v = part[(long long)ch * a.C + c];
+            s += ((double)v.x + (double)v.y) * min(a.rows, n - ch * a.rows);
+        }
     }
-    const double count = (double)n * a.D;
-    const double mean = n > 0 ? block_sum(s, sh) / count : 0.0;
+    const double inv = n > 0 ? 1.0 / ((double)n * a.D) : 0.0;
+    const double mean = block_sum(s, sh) * inv;
     double q = 0;
-    for (long long i = threadIdx.x; i < m; i += kThreads) {
-        const int ch = (int)(i / a.D), c = (int)(i % a.D);
-        const int rows = min(a.rows, n - ch * a.rows);
-        const float4 v = part[(long long)ch * a.C + c];
-        const double d = (double)v.x + (double)v.y - mean;
-        q += (double)v.z + d * d * rows;
+    for (int c = lx; c < a.D; c += tx) {
+#pragma unroll 4
+        for (int ch = ly; ch < used; ch += ny) {
+            const float4 v = part[(long long)ch * a.C + c];
+            const double d = (double)v.x + (double)v.y - mean;
+            q += (double)v.z + d * d * min(a.rows, n - ch * a.rows);
+        }
     }
-    const double var = n > 0 ? block_sum(q, sh) / count : 0.0;
+    const double var = block_sum(q, sh) * inv;
     if (threadIdx.x == 0) {
         a.mean[blockIdx.x] = (float)mean;
-        a.rstd[blockIdx.x] = (float)(1.0 / sqrt(var + (double)a.eps));
+        a.rstd[blockIdx.x] = 1.0f / sqrtf((float)(var + (double)a.eps));
     }
 }
 
 // y = act((x - mean) rstd w + b), zeros behind the valid rows.  Blocks go through the tensor from its
 // end: what the statistics pass read last is still in L2.
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kThreads) k_norm_apply(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const NormArgs a) {
     constexpr bool kPrecise = sizeof(T) == 4, kSnake = ACT == MH3A_ACT_SNAKE_BETA;
     constexpr int H = Acc<V>::H;
     ptx::grid_dep_wait();
@@ -261,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_apply(const NormArgs a) {
         if constexpr (V == 1) *to = from_f<T>(f.v[0].x);
         else store_pairs<T, V>(to, f.v);
     };
-    constexpr int U = 4;
+    constexpr int U = kBatch;
     int k = 0;
     for (; k + U <= mine; k += U) {
         Pack<T, V> in[U];
@@ -278,83 +287,107 @@ __global__ void __launch_bounds__(kThreads) k_norm_apply(const NormArgs a) {
 }
 
 // --------------------------------------------------------------------------------- backward
-// Sums of one channel: 0 du, 1 du xh, 2 dy * (factor of dalpha), 3 dy * (factor of dbeta).
-template <int ACT>
-constexpr int kSums = ACT == MH3A_ACT_SNAKE_BETA ? 4 : 2;
+
+// The per-channel parameters of a thread, as pairs.
+template <int V, int ACT>
+struct BwdParams {
+    static constexpr int H = Acc<V>::H;
+    float2 mu[H], rs[H], w[H], bi[H], al[H], ib[H];
+
+    __device__ __forceinline__ void load(const NormArgs& a, int b, int c0) {
+        float* f[6] = {&mu[0].x, &rs[0].x, &w[0].x, &bi[0].x, &al[0].x, &ib[0].x};
+#pragma unroll
+        for (int i = 0; i < 2 * H; ++i) {
+            const int c = min(c0 + i, a.C - 1);
+            const long long g = (long long)b * a.G + c / a.D;
+            f[0][i] = -a.mean[g];
+            f[1][i] = a.rstd[g];
+            f[2][i] = a.weight ? __ldg(a.weight + c) : 1.f;
+            f[3][i] = a.bias ? __ldg(a.bias + c) : 0.f;
+            if (ACT == MH3A_ACT_SNAKE_BETA) {
+                f[4][i] = __ldg(a.alpha + c);
+                f[5][i] = rcp_ftz(__ldg(a.beta + c) + 1e-9f);
+            }
+        }
+    }
+    __device__ __forceinline__ float2 xhat(float2 x, int i) const { return __fmul2_rn(__fadd2_rn(x, mu[i]), rs[i]); }
+    template <bool PRECISE>
+    __device__ __forceinline__ float2 slope(float2 xh, int i, float2* pa, float2* pb) const {
+        constexpr bool kSnake = ACT == MH3A_ACT_SNAKE_BETA;
+        const float2 u = __ffma2_rn(xh, w[i], bi[i]);
+        return act_slope2<ACT, PRECISE>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u, pa, pb);
+    }
+};
 
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kThreads) k_norm_bwd_partial(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_norm_bwd_partial(const NormArgs a) {
     constexpr bool kPrecise = sizeof(T) == 4;
-    constexpr int NS = kSums<ACT>;
+    constexpr int NS = kSums<ACT>, H = Acc<V>::H;
     ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
     const Place p = place<V>(a, blockIdx.x);
     const int n = valid_rows(a, p.b);
     const int r0 = min(p.ch * a.rows, n), r1 = min(r0 + a.rows, n);
-    float acc[V][NS];
+    float2 acc[NS][H];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int j = 0; j < NS; ++j)
 #pragma unroll
-        for (int j = 0; j < NS; ++j) acc[i][j] = 0.f;
+        for (int i = 0; i < H; ++i) acc[j][i] = make_float2(0.f, 0.f);
     if (p.live) {
-        float mu[V], rs[V], w[V], bi[V], al[V], ib[V];
-        load_param<V>(a.weight, p.c, a.C, 1.f, w);
-        load_param<V>(a.bias, p.c, a.C, 0.f, bi);
-        if (ACT == MH3A_ACT_SNAKE_BETA) {
-            load_param<V>(a.alpha, p.c, a.C, 0.f, al);
-            load_param<V>(a.beta, p.c, a.C, 0.f, ib);
-        }
+        BwdParams<V, ACT> prm;
+        prm.load(a, p.b, p.c);
+        const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c + (long long)(r0 + p.ty) * a.xr;
+        const T* dy = static_cast<const T*>(a.dy) + p.b * a.gb + p.c + (long long)(r0 + p.ty) * a.gr;
+        const long long xs = (long long)p.TY * a.xr, gs = (long long)p.TY * a.gr;
+        const int mine = r1 - r0 > p.ty ? (r1 - r0 - p.ty + p.TY - 1) / p.TY : 0;
+        auto add = [&](const Pack<T, V>& in, const Pack<T, V>& gr) {
+            Acc<V> f, g;
+            unpack_acc<T, V>(in, f);
+            unpack_acc<T, V>(gr, g);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int g = p.b * a.G + min(p.c + i, a.C - 1) / a.D;
-            mu[i] = a.mean[g];
-            rs[i] = a.rstd[g];
-            if (ACT == MH3A_ACT_SNAKE_BETA) ib[i] = 1.0f / (ib[i] + 1e-9f);
-        }
-        const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c;
-        const T* dy = static_cast<const T*>(a.dy) + p.b * a.gb + p.c;
-        constexpr int U = 4;
-        for (int t = r0 + p.ty; t < r1; t += U * p.TY) {
-            Pack<T, V> in[U], gr[U];
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int row = t + k * p.TY;
-                if (row < r1) {
-                    in[k] = load_pack<T, V>(x + (long long)row * a.xr);
-                    gr[k] = load_pack<T, V>(dy + (long long)row * a.gr);
+            for (int i = 0; i < H; ++i) {
+                const float2 xh = prm.xhat(f.v[i], i);
+                float2 pa, pb;
+                const float2 du = __fmul2_rn(g.v[i], prm.template slope<kPrecise>(xh, i, &pa, &pb));
+                acc[0][i] = __fadd2_rn(acc[0][i], du);
+                acc[1][i] = __ffma2_rn(du, xh, acc[1][i]);
+                if constexpr (NS == 4) {
+                    acc[2][i] = __ffma2_rn(g.v[i], pa, acc[2][i]);
+                    acc[3][i] = __ffma2_rn(g.v[i], pb, acc[3][i]);
                 }
             }
+        };
+        int k = 0;
+        for (; k + kBatch <= mine; k += kBatch) {
+            Pack<T, V> in[kBatch], gr[kBatch];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                if (t + k * p.TY >= r1) break;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float xh = (to_f<T>(in[k].v[i]) - mu[i]) * rs[i];
-                    const float g = to_f<T>(gr[k].v[i]);
-                    float pa = 0.f, pb = 0.f;
-                    const float du = g * act_slope<ACT, kPrecise>(fmaf(xh, w[i], bi[i]), ACT == MH3A_ACT_SNAKE_BETA ? al[i] : 0.f,
-                                                                  ACT == MH3A_ACT_SNAKE_BETA ? ib[i] : 0.f, &pa, &pb);
-                    acc[i][0] += du;
-                    acc[i][1] = fmaf(du, xh, acc[i][1]);
-                    if constexpr (NS == 4) {
-                        acc[i][2] = fmaf(g, pa, acc[i][2]);
-                        acc[i][3] = fmaf(g, pb, acc[i][3]);
-                    }
-                }
+            for (int j = 0; j < kBatch; ++j) {
+                in[j] = load_pack<T, V>(x + j * xs);
+                gr[j] = load_pack<T, V>(dy + j * gs);
             }
+            x += kBatch * xs;
+            dy += kBatch * gs;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) add(in[j], gr[j]);
         }
+        for (; k < mine; ++k, x += xs, dy += gs) add(load_pack<T, V>(x), load_pack<T, V>(dy));
     }
     for (int off = 16; off >= a.tx; off >>= 1) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int j = 0; j < NS; ++j)
 #pragma unroll
-            for (int j = 0; j < NS; ++j) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], off);
+            for (int i = 0; i < H; ++i) {
+                acc[j][i].x += __shfl_xor_sync(0xffffffffu, acc[j][i].x, off);
+                acc[j][i].y += __shfl_xor_sync(0xffffffffu, acc[j][i].y, off);
+            }
     }
     __shared__ float sm[kThreads / 32][32 * V * NS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto part = [&](int i, int j) { return V == 1 || i % 2 == 0 ? acc[j][i / 2].x : acc[j][i / 2].y; };
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < NS; ++j) sm[warp][(i * NS + j) * 32 + lane] = acc[i][j];
+        for (int j = 0; j < NS; ++j) sm[warp][(i * NS + j) * 32 + lane] = part(i, j);
     __syncthreads();
     if (warp == 0 && lane < a.tx && p.live) {
         float* out = a.ws + (((long long)p.b * a.chunks + p.ch) * a.C + p.c) * NS;
@@ -433,81 +466,84 @@ __global__ void __launch_bounds__(256) k_norm_bwd_final(const NormArgs a, const 
     }
 }
 
+// dx, from the tensor's end as in k_norm_apply.
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(const NormArgs a, const float2* means) {
+__global__ void __launch_bounds__(kThreads, 3) k_norm_bwd_apply(const NormArgs a, const float2* means) {
     constexpr bool kPrecise = sizeof(T) == 4;
+    constexpr int H = Acc<V>::H;
     ptx::grid_dep_wait();
-    const Place p = place<V>(a, blockIdx.x);
+    const Place p = place<V>(a, gridDim.x - 1 - blockIdx.x);
     if (!p.live) return;
     const int n = valid_rows(a, p.b);
     const int r0 = min(p.ch * a.rows, a.T), r1 = min(r0 + a.rows, a.T);
-    float mu[V], rs[V], w[V], bi[V], al[V], ib[V], m1[V], m2[V];
-    load_param<V>(a.weight, p.c, a.C, 1.f, w);
-    load_param<V>(a.bias, p.c, a.C, 0.f, bi);
-    if (ACT == MH3A_ACT_SNAKE_BETA) {
-        load_param<V>(a.alpha, p.c, a.C, 0.f, al);
-        load_param<V>(a.beta, p.c, a.C, 0.f, ib);
-    }
+    BwdParams<V, ACT> prm;
+    prm.load(a, p.b, p.c);
+    float2 m1[H], m2[H];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int g = p.b * a.G + min(p.c + i, a.C - 1) / a.D;
-        mu[i] = a.mean[g];
-        rs[i] = a.rstd[g];
-        m1[i] = means[g].x;
-        m2[i] = means[g].y;
-        if (ACT == MH3A_ACT_SNAKE_BETA) ib[i] = 1.0f / (ib[i] + 1e-9f);
+    for (int i = 0; i < H; ++i) {
+        const float2 f = means[(long long)p.b * a.G + min(p.c + 2 * i, a.C - 1) / a.D];
+        const float2 h = means[(long long)p.b * a.G + min(p.c + 2 * i + 1, a.C - 1) / a.D];
+        m1[i] = make_float2(-f.x, -h.x);
+        m2[i] = make_float2(-f.y, -h.y);
     }
-    const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c;
-    const T* dy = static_cast<const T*>(a.dy) + p.b * a.gb + p.c;
-    T* dx = static_cast<T*>(a.out) + (long long)p.b * a.T * a.C + p.c;
-    constexpr int U = 2;
-    for (int t = r0 + p.ty; t < r1; t += U * p.TY) {
-        Pack<T, V> in[U], gr[U];
+    const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c + (long long)(r0 + p.ty) * a.xr;
+    const T* dy = static_cast<const T*>(a.dy) + p.b * a.gb + p.c + (long long)(r0 + p.ty) * a.gr;
+    T* dx = static_cast<T*>(a.out) + ((long long)p.b * a.T + r0 + p.ty) * a.C + p.c;
+    const long long xs = (long long)p.TY * a.xr, gs = (long long)p.TY * a.gr, os = (long long)p.TY * a.C;
+    const int top = min(n, r1) - r0;
+    const int mine = top > p.ty ? (top - p.ty + p.TY - 1) / p.TY : 0;
+    auto put = [&](const Pack<T, V>& in, const Pack<T, V>& gr, T* to) {
+        Acc<V> f, g;
+        unpack_acc<T, V>(in, f);
+        unpack_acc<T, V>(gr, g);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int row = t + k * p.TY;
-            if (row < r1 && row < n) {
-                in[k] = load_pack<T, V>(x + (long long)row * a.xr);
-                gr[k] = load_pack<T, V>(dy + (long long)row * a.gr);
-            }
+        for (int i = 0; i < H; ++i) {
+            const float2 xh = prm.xhat(f.v[i], i);
+            float2 pa, pb;
+            const float2 du = __fmul2_rn(g.v[i], prm.template slope<kPrecise>(xh, i, &pa, &pb));
+            f.v[i] = __fmul2_rn(prm.rs[i], __ffma2_rn(xh, m2[i], __ffma2_rn(du, prm.w[i], m1[i])));
         }
+        if constexpr (V == 1) *to = from_f<T>(f.v[0].x);
+        else store_pairs<T, V>(to, f.v);
+    };
+    int k = 0;
+    for (; k + kBatch <= mine; k += kBatch) {
+        Pack<T, V> in[kBatch], gr[kBatch];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int row = t + k * p.TY;
-            if (row >= r1) break;
-            float f[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                f[i] = 0.f;
-                if (row < n) {
-                    const float xh = (to_f<T>(in[k].v[i]) - mu[i]) * rs[i];
-                    float pa, pb;
-                    const float du = to_f<T>(gr[k].v[i]) *
-                                     act_slope<ACT, kPrecise>(fmaf(xh, w[i], bi[i]), ACT == MH3A_ACT_SNAKE_BETA ? al[i] : 0.f,
-                                                              ACT == MH3A_ACT_SNAKE_BETA ? ib[i] : 0.f, &pa, &pb);
-                    f[i] = rs[i] * (fmaf(du, w[i], -m1[i]) - xh * m2[i]);
-                }
-            }
-            store_pack<T, V>(dx + (long long)row * a.C, f);
+        for (int j = 0; j < kBatch; ++j) {
+            in[j] = load_pack<T, V>(x + j * xs);
+            gr[j] = load_pack<T, V>(dy + j * gs);
         }
+        x += kBatch * xs;
+        dy += kBatch * gs;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) put(in[j], gr[j], dx + j * os);
+        dx += kBatch * os;
     }
+    for (; k < mine; ++k, x += xs, dy += gs, dx += os) put(load_pack<T, V>(x), load_pack<T, V>(dy), dx);
+    const Pack<T, V> zero{};
+    for (; p.ty + k * p.TY < r1 - r0; ++k, dx += os) *reinterpret_cast<Pack<T, V>*>(dx) = zero;
 }
 
 // ------------------------------------------------------------------------------------- host
+constexpr int kFwdPerSm = 4, kBwdPerSm = 8;
+
 int pow2_ceil(long long n, int most) {
     int p = 1;
     while (p < n && p < most) p <<= 1;
     return p;
 }
 
-// Threads, channel tiles and row chunks for vectors of V channels.  Chunks are as many as fill
-// the GPU about `waves` times over, but of at least 4 rows a thread.
-void plan_general(NormArgs* a, int V) {
+// Threads, channel tiles and row chunks for vectors of V channels.  Chunks are as many as give every
+// SM `per_sm` blocks, but of at least 4 rows a thread.  Measured on sixteen 20 s items (256 channels,
+// bf16): forward 100 us with 4, 106 with 8, 110 with 12; backward with unequal lengths, where blocks
+// behind an item's end have nothing to do, 117, 112 and 115.
+void plan_general(NormArgs* a, int V, int per_sm) {
     const long long cvecs = ((long long)a->C + V - 1) / V;
     a->tx = pow2_ceil(cvecs, 32);
     a->ctiles = (int)((cvecs + a->tx - 1) / a->tx);
     const int ty = kThreads / a->tx;
-    const long long want = std::max<long long>(1, 8LL * kSms / std::max<long long>(1, (long long)a->ctiles * a->B));
+    const long long want = std::max<long long>(1, (long long)per_sm * kSms / std::max<long long>(1, (long long)a->ctiles * a->B));
     const long long most = std::max<long long>(1, ((long long)a->T + 4 * ty - 1) / (4 * ty));
     a->chunks = (int)std::min(want, most);
     a->rows = (a->T + a->chunks - 1) / a->chunks;
@@ -523,7 +559,11 @@ bool go(F kern, long long grid, int threads, cudaStream_t s, Args... args) {
 
 // Shared memory of a resident block: two blocks an SM where the slab allows, else one.
 constexpr int kResTwo = 112 * 1024, kResOne = 224 * 1024;
-static const long long kResMax = (getenv("RMAX") ? atoi(getenv("RMAX")) : 16) * 1000000LL;
+// Larger tensors take the general form: a cluster's slab is a 64- or 128-byte piece of every row, and
+// once clusters drift apart the pieces of a row reach DRAM at different times.  Measured (bf16, forward,
+// T = 10000, C = 256): 41 MB 27 us against 33 us in the general form, 164 MB (T = 20000) 101 against 100;
+// backward (x and dy) 82 MB 62 against 82 us, 164 MB 145 against 125.
+constexpr long long kResMax = 100000000LL;
 
 FastDiv fast_div(unsigned d) { return FastDiv{d, (unsigned)(((1ull << 32) + d - 1) / d)}; }
 
@@ -588,7 +628,7 @@ template <typename T, int V>
 bool forward_general(const NormArgs& a, int act, cudaStream_t s) {
     const long long grid = grid_general(a);
     if (!go(k_norm_partial<T, V>, grid, kThreads, s, a)) return false;
-    if (!go(k_norm_stats, (long long)a.B * a.G, kThreads, s, a)) return false;
+    if (!go(k_norm_stats, (long long)a.B * a.G, kStatThreads, s, a, pow2_ceil(a.D, kStatThreads))) return false;
     switch (act) {
         case MH3A_ACT_SILU: return go(k_norm_apply<T, V, MH3A_ACT_SILU>, grid, kThreads, s, a);
         case MH3A_ACT_SNAKE_BETA: return go(k_norm_apply<T, V, MH3A_ACT_SNAKE_BETA>, grid, kThreads, s, a);
@@ -608,7 +648,7 @@ bool forward(NormArgs& a, int act, bool vec, cudaStream_t s) {
             default: return forward_resident<T, V, MH3A_ACT_NONE>(a, r, s);
         }
     }
-    plan_general(&a, vec ? V : 1);
+    plan_general(&a, vec ? V : 1, kFwdPerSm);
     return vec ? forward_general<T, V>(a, act, s) : forward_general<T, 1>(a, act, s);
 }
 
@@ -626,12 +666,29 @@ bool backward_general(const NormArgs& a, cudaStream_t s) {
     return go(k_norm_bwd_apply<T, V, ACT>, grid, kThreads, s, a, (const float2*)means);
 }
 
-template <typename T, int V>
-bool backward_act(const NormArgs& a, int act, cudaStream_t s) {
+template <typename T, int ACT>
+bool backward_act(NormArgs& a, bool vec, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T), NS = kSums<ACT>;
+    Resident r;
+    auto extra = [&](int W, int S) { return res_bwd_extra(W, a.D, V, S, NS); };
+    if (vec && plan_resident(a, V, sizeof(T), 2 * sizeof(T), extra, &r)) {
+        const bool ok = a.D % V == 0 ? go_resident(k_norm_bwd_resident<T, V, ACT, true>, a, r, s)
+                                     : go_resident(k_norm_bwd_resident<T, V, ACT, false>, a, r, s);
+        if (!ok || a.B == 1) return ok;
+        return go(k_norm_bwd_final, (a.C + 255LL) / 256, 256, s, a, (const float*)a.ws, (float2*)nullptr, NS, 0);
+    }
+    // 8-byte vectors for 16-bit types: twice as many channels' sums and parameters would halve the blocks
+    // an SM holds
+    plan_general(&a, vec ? 4 : 1, kBwdPerSm);
+    return vec ? backward_general<T, 4, ACT>(a, s) : backward_general<T, 1, ACT>(a, s);
+}
+
+template <typename T>
+bool backward(NormArgs& a, int act, bool vec, cudaStream_t s) {
     switch (act) {
-        case MH3A_ACT_SILU: return backward_general<T, V, MH3A_ACT_SILU>(a, s);
-        case MH3A_ACT_SNAKE_BETA: return backward_general<T, V, MH3A_ACT_SNAKE_BETA>(a, s);
-        default: return backward_general<T, V, MH3A_ACT_NONE>(a, s);
+        case MH3A_ACT_SILU: return backward_act<T, MH3A_ACT_SILU>(a, vec, s);
+        case MH3A_ACT_SNAKE_BETA: return backward_act<T, MH3A_ACT_SNAKE_BETA>(a, vec, s);
+        default: return backward_act<T, MH3A_ACT_NONE>(a, vec, s);
     }
 }
 
@@ -665,13 +722,13 @@ NormArgs base_args(const mh3a_norm* p) {
     return a;
 }
 
-// Scratch of the general form.  Scalar plans (V = 1) never have more chunks than vector plans
-// for the same tensor have room for, but the layouts differ, so the size is the larger of both.
+// Scratch of the general form, the largest over its vector widths; the resident form needs less (the
+// per-channel sums of each item).
 size_t general_bytes(const mh3a_norm* p, int backward) {
     size_t most = 0;
-    for (int V : {1, 16 / elem_bytes(p->dtype)}) {
+    for (int V : {1, 4, 16 / elem_bytes(p->dtype)}) {
         NormArgs a = base_args(p);
-        plan_general(&a, V);
+        plan_general(&a, V, backward ? kBwdPerSm : kFwdPerSm);
         const long long ns = p->act == MH3A_ACT_SNAKE_BETA ? 4 : 2;
         long long floats = (long long)a.B * a.chunks * a.C * (backward ? ns : 4);
         if (backward) floats += ((long long)a.B * a.C * ns + 3) / 4 * 4 + 2LL * a.B * a.G;
@@ -756,13 +813,12 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p,
     a.ws = static_cast<float*>(workspace);
     const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(dx, 16) &&
                      strides_fit(a.xb, a.xr, V) && strides_fit(a.gb, a.gr, V) && params_fit(a);
-    plan_general(&a, vec ? V : 1);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     bool ok;
     switch (p->dtype) {
-        case MH3A_DTYPE_F32: ok = vec ? backward_act<float, 4>(a, p->act, s) : backward_act<float, 1>(a, p->act, s); break;
-        case MH3A_DTYPE_F16: ok = vec ? backward_act<__half, 8>(a, p->act, s) : backward_act<__half, 1>(a, p->act, s); break;
-        default: ok = vec ? backward_act<__nv_bfloat16, 8>(a, p->act, s) : backward_act<__nv_bfloat16, 1>(a, p->act, s);
+        case MH3A_DTYPE_F32: ok = backward<float>(a, p->act, vec, s); break;
+        case MH3A_DTYPE_F16: ok = backward<__half>(a, p->act, vec, s); break;
+        default: ok = backward<__nv_bfloat16>(a, p->act, vec, s);
     }
     return ok ? MH3A_OK : launch_failed("mh3a_group_norm_act_backward");
 }

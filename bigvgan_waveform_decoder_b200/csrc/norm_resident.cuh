@@ -4,9 +4,8 @@
 // where the tensor has them); each block keeps a chunk of the slab's rows in shared memory, so the
 // statistics and the elementwise pass read global memory once and write it once.  The S blocks
 // exchange their partial sums through distributed shared memory: each block stores its own into every
-// peer's inbox with st.async, which counts the bytes on the peer's mbarrier.  A cluster barrier in
-// its place would wait for the block's outstanding output stores (measured: 202 us against XXX at
-// the batch of sixteen 20 s items, 256 channels, bf16).  A thread reads back only what it
+// peer's inbox with st.async, which counts the bytes on the peer's mbarrier (a cluster barrier with
+// loads from the peers in its place took 7.7 us against 6.8 at [2, 2000, 512]).  A thread reads back only what it
 // copied itself (its channels are fixed, its rows are every TY-th), so no barrier stands between the
 // copies and their use, and the statistics of the rows that have arrived are formed while the later
 // ones are on their way.
@@ -288,6 +287,228 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
         }
         const Pack<T, V> zero{};  // rows behind the item's length
         for (int k = mine; p.ty + k * p.TY < r1 - r0; ++k, y += step) *reinterpret_cast<Pack<T, V>*>(y) = zero;
+    }
+}
+
+// Backward: shared memory behind x and dy: the threads' per-channel sums (one row for each warp where
+// shuffles put the warp's rows together, else for each row of threads), the inbox of every peer's sums,
+// their totals, and the groups' two means.
+__host__ __device__ constexpr int res_bwd_extra(int W, int D, int V, int S, int ns) {
+    return kResThreads * V * ns * 4 + (S + 1) * W * ns * 4 + (W / D) * 8 + 16;
+}
+
+// dx and the per-channel sums of one item's slab.  `a.ws` takes the item's totals [B][C][NS]; with one
+// item they are the parameter gradients already.
+template <typename T, int V, int ACT, bool WHOLE>
+__global__ void __launch_bounds__(kResThreads) k_norm_bwd_resident(const NormArgs a, const Resident r) {
+    constexpr bool kPrecise = sizeof(T) == 4;
+    constexpr int H = V / 2, NS = kSums<ACT>, M = WHOLE ? 1 : H;
+    constexpr bool kSnake = ACT == MH3A_ACT_SNAKE_BETA;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const ResPlace p = res_place<V>(r);
+    const int r0 = min(p.rank * r.rows, a.T), r1 = min(r0 + r.rows, a.T);
+    const int ng = (unsigned)r.W / r.D, cols = r.W * NS;
+    const uint32_t bytes = (uint32_t)r.rows * r.W * sizeof(T);
+    float* red = reinterpret_cast<float*>(smem + 2 * (size_t)bytes);
+    float* inbox = red + kResThreads * V * NS;  // [S][cols]
+    float* total = inbox + r.S * cols;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(total + cols);
+    float2* fin = reinterpret_cast<float2*>(bar + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int next = p.TY * p.w;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(bar, 1);
+        ptx::fence_mbar_init();
+        ptx::mbar_arrive_expect_tx(bar, r.S * cols * 4);
+    }
+    cluster_arrive();
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int n = valid_rows(a, p.b);
+    const int have = max(0, min(n, r1) - r0);
+    const int mine = p.live && have > p.ty ? (int)((unsigned)(have - p.ty + p.TY - 1) / r.ty) : 0;
+    const int per = (mine + kParts - 1) / kParts;
+    const int first = p.tx + p.ty * p.w;
+    {
+        const T* x = static_cast<const T*>(a.x) + p.b * a.xb + p.c + (long long)(r0 + p.ty) * a.xr;
+        const T* dy = static_cast<const T*>(a.dy) + p.b * a.gb + p.c + (long long)(r0 + p.ty) * a.gr;
+        const long long xs = (long long)p.TY * a.xr, gs = (long long)p.TY * a.gr;
+        uint32_t to = ptx::smem_u32(smem) + first * 16;
+        int k = 0;
+#pragma unroll
+        for (int g = 0; g < kParts; ++g) {
+#pragma unroll 2
+            for (int e = min(mine, (g + 1) * per); k < e; ++k, x += xs, dy += gs, to += next * 16) {
+                cp_async16_to(to, x);
+                cp_async16_to(to + bytes, dy);
+            }
+            ptx::cp_async_commit();
+        }
+    }
+    float2 mu[M], rs[M], w[H], bi[H], al[H], ib[H];
+    if (p.live) {
+        load_param_vec<V>(a.weight, p.c, 1.f, w);
+        load_param_vec<V>(a.bias, p.c, 0.f, bi);
+        if (kSnake) {
+            load_param_vec<V>(a.alpha, p.c, 0.f, al);
+            load_param_vec<V>(a.beta, p.c, 0.f, ib);
+#pragma unroll
+            for (int i = 0; i < H; ++i) ib[i] = make_float2(rcp_ftz(ib[i].x + 1e-9f), rcp_ftz(ib[i].y + 1e-9f));
+        }
+        const long long g0 = (long long)p.b * a.G + p.c0 / a.D;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const int ga = (unsigned)(p.tx * V + 2 * i) / r.D, gb = WHOLE ? ga : (unsigned)(p.tx * V + 2 * i + 1) / r.D;
+            mu[i] = make_float2(-a.mean[g0 + ga], -a.mean[g0 + gb]);
+            rs[i] = make_float2(a.rstd[g0 + ga], a.rstd[g0 + gb]);
+        }
+    }
+    Pack<T, V>* myx = reinterpret_cast<Pack<T, V>*>(smem) + first;
+    Pack<T, V>* myg = reinterpret_cast<Pack<T, V>*>(smem + bytes) + first;
+
+    float2 acc[NS][H];
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+        for (int i = 0; i < H; ++i) acc[j][i] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int g = 0; g < kParts; ++g) {
+        if (g == 0) cp_async_wait_group<kParts - 1>();
+        if (g == 1) cp_async_wait_group<kParts - 2>();
+        if (g == 2) cp_async_wait_group<kParts - 3>();
+        if (g == 3) cp_async_wait_group<kParts - 4>();
+        for (int k = g * per, e = min(mine, (g + 1) * per); k < e; ++k) {
+            float2 f[H], d[H];
+            unpack_pairs<T, V>(myx[k * next], f);
+            unpack_pairs<T, V>(myg[k * next], d);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float2 xh = __fmul2_rn(__fadd2_rn(f[i], mu[WHOLE ? 0 : i]), rs[WHOLE ? 0 : i]);
+                const float2 u = __ffma2_rn(xh, w[i], bi[i]);
+                float2 pa, pb;
+                const float2 du = __fmul2_rn(d[i], act_slope2<ACT, kPrecise>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u, &pa, &pb));
+                acc[0][i] = __fadd2_rn(acc[0][i], du);
+                acc[1][i] = __ffma2_rn(du, xh, acc[1][i]);
+                if constexpr (NS == 4) {
+                    acc[2][i] = __ffma2_rn(d[i], pa, acc[2][i]);
+                    acc[3][i] = __ffma2_rn(d[i], pb, acc[3][i]);
+                }
+                if (kPrecise) d[i] = du;  // fp32: kept in dy's place, exactly what the second pass needs
+            }
+            if (kPrecise && ACT != MH3A_ACT_NONE) store_pairs<T, V>(reinterpret_cast<T*>(myg + k * next), d);
+        }
+    }
+    // the block's sums: lanes that share channels first, where they stand a power of two apart
+    const bool shuffled = p.w < 32 && (p.w & (p.w - 1)) == 0;
+    int nrow = p.TY, row = p.ty;
+    bool put = p.live;
+    if (shuffled) {
+        for (int off = 16; off >= p.w; off >>= 1) {
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    acc[j][i].x += __shfl_xor_sync(0xffffffffu, acc[j][i].x, off);
+                    acc[j][i].y += __shfl_xor_sync(0xffffffffu, acc[j][i].y, off);
+                }
+        }
+        nrow = kResThreads / 32;
+        row = warp;
+        put = lane < p.w;
+    }
+    if (put) {
+        float* to = red + row * cols + p.tx * V;  // [sum][channel]
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int i = 0; i < H; ++i) *reinterpret_cast<float2*>(to + j * r.W + 2 * i) = acc[j][i];
+    }
+    __syncthreads();
+    cluster_wait();
+    for (int c = threadIdx.x * 4; c < cols; c += kResThreads * 4) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < nrow; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(red + k * cols + c);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        for (int peer = 0; peer < r.S; ++peer)
+            send16(peer_smem(ptx::smem_u32(inbox + p.rank * cols + c), peer), peer_smem(ptx::smem_u32(bar), peer), s);
+    }
+    const bool arrived = ptx::mbar_wait(bar, 0);
+    for (int c = threadIdx.x; c < cols; c += kResThreads) {
+        float s = 0.f;
+        for (int k = 0; k < r.S; ++k) s += inbox[k * cols + c];
+        total[c] = arrived ? s : __int_as_float(0x7fffffff);
+    }
+    __syncthreads();
+    for (int g = warp; g < ng; g += kResThreads / 32) {
+        float s1 = 0.f, s2 = 0.f;
+        for (int i = lane; i < a.D; i += 32) {
+            const int c = g * a.D + i;
+            const float wc = a.weight ? __ldg(a.weight + p.c0 + c) : 1.f;
+            s1 = fmaf(wc, total[c], s1);
+            s2 = fmaf(wc, total[r.W + c], s2);
+        }
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        const float inv = n > 0 ? 1.0f / ((float)n * a.D) : 0.f;
+        if (lane == 0) fin[g] = make_float2(-s1 * inv, -s2 * inv);
+    }
+    if (p.rank == 0) {
+        for (int c = threadIdx.x; c < r.W; c += kResThreads) {
+            const int at = p.c0 + c;
+            if (a.B == 1) {
+                if (a.dbias) a.dbias[at] = total[c];
+                if (a.dweight) a.dweight[at] = total[r.W + c];
+                if constexpr (NS == 4) {
+                    if (a.dalpha) a.dalpha[at] = total[2 * r.W + c];
+                    if (a.dbeta) {
+                        const float v = 1.0f / (a.beta[at] + 1e-9f);
+                        a.dbeta[at] = -total[3 * r.W + c] * v * v;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NS; ++j) a.ws[((long long)p.b * a.C + at) * NS + j] = total[j * r.W + c];
+            }
+        }
+    }
+    __syncthreads();
+    if (p.live) {
+        float2 m1[M], m2[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const float2 f = fin[(unsigned)(p.tx * V + 2 * i) / r.D];
+            const float2 h = WHOLE ? f : fin[(unsigned)(p.tx * V + 2 * i + 1) / r.D];
+            m1[i] = make_float2(f.x, h.x);
+            m2[i] = make_float2(f.y, h.y);
+        }
+        T* dx = static_cast<T*>(a.out) + ((long long)p.b * a.T + r0 + p.ty) * a.C + p.c;
+        const long long step = (long long)p.TY * a.C;
+        int k = 0;
+        for (; k < mine; ++k, dx += step) {
+            float2 f[H], d[H];
+            unpack_pairs<T, V>(myx[k * next], f);
+            unpack_pairs<T, V>(myg[k * next], d);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const int j = WHOLE ? 0 : i;
+                const float2 xh = __fmul2_rn(__fadd2_rn(f[i], mu[j]), rs[j]);
+                float2 du = d[i];
+                if (!kPrecise) {
+                    const float2 u = __ffma2_rn(xh, w[i], bi[i]);
+                    float2 pa, pb;
+                    du = __fmul2_rn(du, act_slope2<ACT, kPrecise>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u, &pa, &pb));
+                }
+                f[i] = __fmul2_rn(rs[j], __ffma2_rn(xh, m2[j], __ffma2_rn(du, w[i], m1[j])));
+            }
+            store_pairs<T, V>(dx, f);
+        }
+        const Pack<T, V> zero{};
+        for (; p.ty + k * p.TY < r1 - r0; ++k, dx += step) *reinterpret_cast<Pack<T, V>*>(dx) = zero;
     }
 }
 

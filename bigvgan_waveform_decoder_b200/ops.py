@@ -46,84 +46,82 @@ def _load():
     return _lib
 
 
-def _require(ok, what, detail, status=INVALID):
-    if not ok:
-        raise MH3AError(status, what, detail)
+def _bad(what, detail, status=INVALID):
+    return MH3AError(status, what, detail)
 
 
-class _Launch:
-    """The device and stream of a call.  Inside the block the device is current and torch allocates
-    on the call's stream; tensors that cross between that stream and the caller's are recorded."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, device, stream):
-        self.device = device
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.current = torch.cuda.current_stream(device)
+
+def _launch(device, stream, call, inputs):
+    """call(cudaStream_t) -> outputs, with the device current and torch allocating on the call's stream.
+    Tensors that cross between that stream and the caller's are recorded with the allocator."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(_raw_stream(device.index))
+    with torch.cuda.device(device):
+        current = torch.cuda.current_stream()
         if stream is None:
-            stream = self.current
+            stream = current
         elif not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(stream, device=device)
-        self.stream = stream
-        self.ptr = stream.cuda_stream
-        self.side = None if self.ptr == self.current.cuda_stream else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        if self.side is not None:
-            self.side.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.side is not None:
-            self.side.__exit__(*exc)
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def crossing(self, inputs, outputs):
-        if self.side is not None:
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(self.stream)
-            for t in outputs:
-                if t is not None:
-                    t.record_stream(self.current)
+        if stream.cuda_stream == current.cuda_stream:
+            return call(current.cuda_stream)
+        with torch.cuda.stream(stream):
+            outputs = call(stream.cuda_stream)
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+        for t in outputs:
+            if t is not None:
+                t.record_stream(current)
+        return outputs
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _same_device(what, device, **tensors):
-    for name, t in tensors.items():
-        _require(t is None or (isinstance(t, torch.Tensor) and t.device == device), what, f"{name} is not on {device}")
+def _check_frames(what, name, x):
+    if not (isinstance(x, torch.Tensor) and x.is_cuda):
+        raise _bad(what, f"{name} is not a CUDA tensor")
+    if x.dim() != 3:
+        raise _bad(what, f"{name} is not [B, T, C]", SHAPE)
+    if x.dtype not in DTYPES:
+        raise _bad(what, f"{name} has type {x.dtype}")
+    B, T, Cn = x.shape
+    if not (1 <= B < 1 << 31 and 1 <= T < 1 << 31 and 1 <= Cn < 1 << 31):
+        raise _bad(what, f"{name} is empty, or a size passes 2^31", SHAPE)
+    if Cn > 1 and x.stride(2) != 1:
+        raise _bad(what, f"the channels of {name} are not adjacent")
+    return B, T, Cn
 
 
-def _frames(what, name, x):
-    _require(isinstance(x, torch.Tensor) and x.is_cuda, what, f"{name} is not a CUDA tensor")
-    _require(x.dim() == 3, what, f"{name} is not [B, T, C]", SHAPE)
-    _require(x.dtype in DTYPES, what, f"{name} has type {x.dtype}")
-    _require(x.shape[2] <= 1 or x.stride(2) == 1, what, f"the channels of {name} are not adjacent")
-    _require(min(x.shape) >= 1, what, f"{name} is empty", SHAPE)
+def _check_plain(what, name, t, device, dtype, shape):
+    """A contiguous tensor of a type and shape on the call's device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.is_contiguous()):
+        raise _bad(what, f"{name} is not a contiguous {dtype} tensor on {device}")
+    if t.shape != shape:
+        raise _bad(what, f"{name} is not of shape {list(shape)}", SHAPE)
 
 
 def _norm_args(what, x, groups, weight, bias, act, alpha, beta, eps, lengths):
-    _frames(what, "x", x)
-    B, T, Cn = x.shape
-    _require(max(x.shape) < 1 << 31, what, "a size of x passes 2^31", SHAPE)
-    _require(act in ACTS, what, f"unknown activation {act!r}")
-    _require((act == "snake_beta") == (alpha is not None) == (beta is not None), what,
-             "alpha and beta belong to snake_beta, and it needs both")
-    for name, t in (("weight", weight), ("bias", bias), ("alpha", alpha), ("beta", beta)):
-        if t is not None:
-            _require(isinstance(t, torch.Tensor) and t.device == x.device and t.dtype == torch.float32 and t.is_contiguous(),
-                     what, f"{name} is not a contiguous float32 tensor on {x.device}")
-            _require(t.shape == (Cn,), what, f"{name} is not [{Cn}]", SHAPE)
+    B, T, Cn = _check_frames(what, "x", x)
+    if act not in ACTS:
+        raise _bad(what, f"unknown activation {act!r}")
+    if not (act == "snake_beta") == (alpha is not None) == (beta is not None):
+        raise _bad(what, "alpha and beta belong to snake_beta, and it needs both")
+    device, shape = x.device, (Cn,)
+    if weight is not None:
+        _check_plain(what, "weight", weight, device, torch.float32, shape)
+    if bias is not None:
+        _check_plain(what, "bias", bias, device, torch.float32, shape)
+    if alpha is not None:
+        _check_plain(what, "alpha", alpha, device, torch.float32, shape)
+        _check_plain(what, "beta", beta, device, torch.float32, shape)
     if lengths is not None:
-        _require(isinstance(lengths, torch.Tensor) and lengths.device == x.device and lengths.dtype == torch.int32 and
-                 lengths.is_contiguous(), what, f"lengths is not a contiguous int32 tensor on {x.device}")
-        _require(lengths.shape == (B,), what, f"lengths is not [{B}]", SHAPE)
-    _require(isinstance(groups, int) and groups >= 1 and Cn % groups == 0, what, f"{groups} groups do not divide {Cn} channels", SHAPE)
+        _check_plain(what, "lengths", lengths, device, torch.int32, (B,))
+    if not (isinstance(groups, int) and groups >= 1 and Cn % groups == 0):
+        raise _bad(what, f"{groups} groups do not divide {Cn} channels", SHAPE)
     return mh3a_norm(DTYPES[x.dtype], ACTS[act], B, T, Cn, groups, eps, _ptr(weight), _ptr(bias), _ptr(alpha), _ptr(beta),
                      _ptr(lengths))
 
@@ -140,20 +138,22 @@ def group_norm_act(x, groups, weight=None, bias=None, act="none", alpha=None, be
     what = "mh3a_group_norm_act"
     p = _norm_args(what, x, groups, weight, bias, act, alpha, beta, eps, lengths)
     if out is not None:
-        _same_device(what, x.device, out=out)
-        _require(out.dtype == x.dtype and out.is_contiguous(), what, "out is not contiguous or not of x's type")
-        _require(out.shape == x.shape, what, "out is not of x's shape", SHAPE)
+        _check_plain(what, "out", out, x.device, x.dtype, x.shape)
     L = _load()
-    with _Launch(x.device, stream) as on:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        stats = torch.empty((2, p.B, groups), dtype=torch.float32, device=x.device)
-        mean, rstd = stats[0], stats[1]
-        n = L.mh3a_group_norm_act_workspace(C.byref(p), 0)
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-        _check(L.mh3a_group_norm_act(C.byref(p), x.data_ptr(), x.stride(0), x.stride(1), y.data_ptr(), mean.data_ptr(),
-                                     rstd.data_ptr(), ws.data_ptr(), n, on.ptr), what)
-        on.crossing((x, weight, bias, alpha, beta, lengths, out), (y if out is None else None, mean, rstd))
-    return y, mean, rstd
+
+    def call(stream):
+        y = x.new_empty(x.shape) if out is None else out
+        mean = x.new_empty((p.B, groups), dtype=torch.float32)
+        rstd = x.new_empty((p.B, groups), dtype=torch.float32)
+        n = L.mh3a_group_norm_act_workspace(p, 0)
+        ws = x.new_empty(n, dtype=torch.uint8)
+        st = L.mh3a_group_norm_act(p, x.data_ptr(), x.stride(0), x.stride(1), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                   ws.data_ptr(), n, stream)
+        if st:
+            _check(st, what)
+        return y, mean, rstd
+
+    return _launch(x.device, stream, call, (x, weight, bias, alpha, beta, lengths, out))
 
 
 def group_norm_act_backward(dy, x, mean, rstd, groups, weight=None, bias=None, act="none", alpha=None, beta=None,
@@ -164,22 +164,25 @@ def group_norm_act_backward(dy, x, mean, rstd, groups, weight=None, bias=None, a
     parameter that is None."""
     what = "mh3a_group_norm_act_backward"
     p = _norm_args(what, x, groups, weight, bias, act, alpha, beta, 0.0, lengths)
-    _frames(what, "dy", dy)
-    _require(dy.device == x.device and dy.dtype == x.dtype, what, "dy is not of x's type and device")
-    _require(dy.shape == x.shape, what, "dy is not of x's shape", SHAPE)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _require(isinstance(t, torch.Tensor) and t.device == x.device and t.dtype == torch.float32 and t.is_contiguous(), what,
-                 f"{name} is not a contiguous float32 tensor on {x.device}")
-        _require(t.shape == (p.B, groups), what, f"{name} is not [{p.B}, {groups}]", SHAPE)
+    _check_frames(what, "dy", dy)
+    if dy.device != x.device or dy.dtype != x.dtype:
+        raise _bad(what, "dy is not of x's type and device")
+    if dy.shape != x.shape:
+        raise _bad(what, "dy is not of x's shape", SHAPE)
+    _check_plain(what, "mean", mean, x.device, torch.float32, (p.B, groups))
+    _check_plain(what, "rstd", rstd, x.device, torch.float32, (p.B, groups))
     L = _load()
-    with _Launch(x.device, stream) as on:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        grads = torch.empty((4, p.C), dtype=torch.float32, device=x.device)
-        dw, db, da, de = (None if t is None else grads[k] for k, t in enumerate((weight, bias, alpha, beta)))
-        n = L.mh3a_group_norm_act_workspace(C.byref(p), 1)
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-        _check(L.mh3a_group_norm_act_backward(C.byref(p), x.data_ptr(), x.stride(0), x.stride(1), dy.data_ptr(),
-                                              dy.stride(0), dy.stride(1), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
-                                              _ptr(dw), _ptr(db), _ptr(da), _ptr(de), ws.data_ptr(), n, on.ptr), what)
-        on.crossing((dy, x, mean, rstd, weight, bias, alpha, beta, lengths), (dx, grads))
-    return dx, dw, db, da, de
+
+    def call(stream):
+        dx = x.new_empty(x.shape)
+        dw, db, da, de = (None if t is None else torch.empty_like(t) for t in (weight, bias, alpha, beta))
+        n = L.mh3a_group_norm_act_workspace(p, 1)
+        ws = x.new_empty(n, dtype=torch.uint8)
+        st = L.mh3a_group_norm_act_backward(p, x.data_ptr(), x.stride(0), x.stride(1), dy.data_ptr(), dy.stride(0),
+                                            dy.stride(1), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db),
+                                            _ptr(da), _ptr(de), ws.data_ptr(), n, stream)
+        if st:
+            _check(st, what)
+        return dx, dw, db, da, de
+
+    return _launch(x.device, stream, call, (dy, x, mean, rstd, weight, bias, alpha, beta, lengths))
