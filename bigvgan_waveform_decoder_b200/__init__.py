@@ -11,7 +11,7 @@ from .binding import (MH3A_BF16X3, MH3A_FLAG_NO_CLAMP, MH3A_FP32, Decoder, MH3AE
 
 def __getattr__(name):
     # ``ops`` imports torch, which the decoder's binding does without until it gets a tensor.
-    if name in ("group_norm_act", "group_norm_act_backward"):
+    if name in ("group_norm_act", "group_norm_act_backward", "fp8_quantize", "fp8_matmul", "fp8_linear"):
         from . import ops
 
         globals()[name] = getattr(ops, name)

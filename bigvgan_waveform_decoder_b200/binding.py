@@ -29,7 +29,8 @@ EXPORTS = ("mh3a_default_config", "mh3a_config_from_json", "mh3a_create", "mh3a_
            "mh3a_device_bytes", "mh3a_destroy", "mh3a_status_string", "mh3a_last_error",
            "mh3a_stage_uses_tensor_cores", "mh3a_segment_uses_tensor_cores",
            "mh3a_check_device_error",
-           "mh3a_group_norm_act_workspace", "mh3a_group_norm_act", "mh3a_group_norm_act_backward")
+           "mh3a_group_norm_act_workspace", "mh3a_group_norm_act", "mh3a_group_norm_act_backward",
+           "mh3a_fp8_quantize", "mh3a_fp8_matmul", "mh3a_fp8_linear_workspace", "mh3a_fp8_linear")
 
 
 class mh3a_config(C.Structure):

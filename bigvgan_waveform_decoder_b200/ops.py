@@ -1,6 +1,8 @@
 """Operators over channels-last frames on the C ABI of include/mh3a.h (argument marshalling only).
 
 ``group_norm_act`` / ``group_norm_act_backward``: group norm with an activation and its gradient.
+``fp8_quantize`` / ``fp8_matmul`` / ``fp8_linear``: matrices in 8-bit floating point with one scale for each
+block of 128 values, their product, and the linear layer (a pointwise convolution) built of both.
 
 Tensors are CUDA tensors of one device; calls run on that device, on ``stream`` (a torch stream or a
 cudaStream_t; the device's current stream when None).  Results and scratch are allocated on that
@@ -42,6 +44,14 @@ def _load():
         L.mh3a_group_norm_act.restype = i
         L.mh3a_group_norm_act_backward.argtypes = [norm, vp, ll, ll, vp, ll, ll, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.mh3a_group_norm_act_backward.restype = i
+        L.mh3a_fp8_quantize.argtypes = [vp, i, i, i, ll, i, i, vp, ll, vp, vp]
+        L.mh3a_fp8_quantize.restype = i
+        L.mh3a_fp8_matmul.argtypes = [vp, ll, vp, vp, ll, vp, i, i, i, i, vp, i, vp, ll, vp]
+        L.mh3a_fp8_matmul.restype = i
+        L.mh3a_fp8_linear_workspace.argtypes = [i, i]
+        L.mh3a_fp8_linear_workspace.restype = sz
+        L.mh3a_fp8_linear.argtypes = [vp, i, ll, vp, ll, vp, i, i, i, i, vp, vp, ll, vp, sz, vp]
+        L.mh3a_fp8_linear.restype = i
         _lib = L
     return _lib
 
@@ -186,3 +196,136 @@ def group_norm_act_backward(dy, x, mean, rstd, groups, weight=None, bias=None, a
         return dx, dw, db, da, de
 
     return _launch(x.device, stream, call, (dy, x, mean, rstd, weight, bias, alpha, beta, lengths))
+
+
+FP8 = torch.float8_e4m3fn
+BLOCK = 128
+
+
+def _check_matrix(what, name, x, types):
+    if not (isinstance(x, torch.Tensor) and x.is_cuda):
+        raise _bad(what, f"{name} is not a CUDA tensor")
+    if x.dtype not in types:
+        raise _bad(what, f"{name} has type {x.dtype}")
+    if x.dim() != 2:
+        raise _bad(what, f"{name} is not a matrix", SHAPE)
+    rows, cols = x.shape
+    if not (1 <= rows < 1 << 31 and 1 <= cols < 1 << 31):
+        raise _bad(what, f"{name} is empty, or a size passes 2^31", SHAPE)
+    if cols > 1 and x.stride(1) != 1:
+        raise _bad(what, f"the columns of {name} are not adjacent")
+    return rows, cols
+
+
+def _check_stored(what, name, q, scale):
+    """An fp8 matrix and its scales: (rows, cols, row stride in bytes, block rows)."""
+    rows, cols = _check_matrix(what, name, q, (FP8,))
+    stride = q.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+    if stride < cols or stride % 16 or q.data_ptr() % 16:
+        raise _bad(what, f"the rows of {name} do not start on 16-byte boundaries")
+    if not (isinstance(scale, torch.Tensor) and scale.dtype == torch.float32 and scale.device == q.device and scale.is_contiguous()):
+        raise _bad(what, f"the scales of {name} are not a contiguous float32 tensor on {q.device}")
+    kb = -(-cols // BLOCK)
+    if scale.shape == (kb, rows):
+        return rows, cols, stride, 1
+    if scale.shape == (kb, -(-rows // BLOCK)):
+        return rows, cols, stride, BLOCK
+    raise _bad(what, f"the scales of {name} are {list(scale.shape)}: [{kb}, {rows}] or [{kb}, {-(-rows // BLOCK)}] are wanted", SHAPE)
+
+
+def _check_bias_out(what, bias, out, device, shape, dtype):
+    if bias is not None:
+        _check_plain(what, "bias", bias, device, torch.float32, shape[1:])
+    if out is not None:
+        if not (isinstance(out, torch.Tensor) and out.dtype == dtype and out.device == device):
+            raise _bad(what, f"out is not a {dtype} tensor on {device}")
+        if out.shape != shape:
+            raise _bad(what, f"out is not {list(shape)}", SHAPE)
+        if (shape[1] > 1 and out.stride(1) != 1) or (shape[0] > 1 and out.stride(0) < shape[1]):
+            raise _bad(what, "the columns of out are not adjacent, or its rows overlap")
+
+
+def _row_stride(t, cols):
+    return t.stride(0) if t.shape[0] > 1 else cols
+
+
+def fp8_quantize(x, block_rows=1, transpose=False, stream=None):
+    """x [rows, cols] (float32, float16 or bfloat16, columns adjacent) in fp8 with one scale for each block of
+    128 columns and ``block_rows`` rows, 1 (activations, gradients) or 128 (weights); mh3a_fp8_quantize.
+    With ``transpose`` the matrix that is blocked and returned is x transposed.  Returns (q, scale): q
+    float8_e4m3fn, its rows on 16-byte boundaries, scale float32 [ceil(inner / 128), ceil(outer /
+    block_rows)]; an element stands for q times its block's scale."""
+    what = "mh3a_fp8_quantize"
+    rows, cols = _check_matrix(what, "x", x, DTYPES)
+    if block_rows not in (1, BLOCK):
+        raise _bad(what, f"block_rows is {block_rows}: 1 or {BLOCK} are wanted")
+    outer, inner = (cols, rows) if transpose else (rows, cols)
+    L = _load()
+
+    def call(stream):
+        ld = (inner + 15) // 16 * 16
+        buf = x.new_empty((outer, ld), dtype=FP8)
+        scale = x.new_empty((-(-inner // BLOCK), -(-outer // block_rows)), dtype=torch.float32)
+        st = L.mh3a_fp8_quantize(x.data_ptr(), DTYPES[x.dtype], rows, cols, _row_stride(x, cols), block_rows,
+                                 1 if transpose else 0, buf.data_ptr(), ld, scale.data_ptr(), stream)
+        if st:
+            _check(st, what)
+        return (buf if ld == inner else buf[:, :inner]), scale
+
+    return _launch(x.device, stream, call, (x,))
+
+
+def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, bias=None, out=None, stream=None):
+    """a [M, K] times b [N, K] transposed, plus bias [N] (float32), for fp8 matrices as fp8_quantize returns
+    them: a with block_rows 1, b with 1 or 128 (mh3a_fp8_matmul).  Sums are fp32, rounded once to
+    ``out_dtype``.  Returns [M, N] (``out`` if given)."""
+    what = "mh3a_fp8_matmul"
+    M, K, a_stride, a_rows = _check_stored(what, "a", a, a_scale)
+    N, Kb, b_stride, b_rows = _check_stored(what, "b", b, b_scale)
+    if a_rows != 1:
+        raise _bad(what, "a has blocks of 128 rows: block_rows 1 is wanted")
+    if K != Kb:
+        raise _bad(what, f"a has {K} columns and b {Kb}", SHAPE)
+    if a.device != b.device:
+        raise _bad(what, "a and b are on different devices")
+    if out_dtype not in DTYPES:
+        raise _bad(what, f"out_dtype is {out_dtype}")
+    _check_bias_out(what, bias, out, a.device, (M, N), out_dtype)
+    L = _load()
+
+    def call(stream):
+        y = a.new_empty((M, N), dtype=out_dtype) if out is None else out
+        st = L.mh3a_fp8_matmul(a.data_ptr(), a_stride, a_scale.data_ptr(), b.data_ptr(), b_stride, b_scale.data_ptr(), b_rows,
+                               M, N, K, _ptr(bias), DTYPES[out_dtype], y.data_ptr(), _row_stride(y, N), stream)
+        if st:
+            _check(st, what)
+        return (y,)
+
+    return _launch(a.device, stream, call, (a, a_scale, b, b_scale, bias, out))[0]
+
+
+def fp8_linear(x, w, w_scale, bias=None, out=None, stream=None):
+    """x [M, K] times w [N, K] transposed, plus bias: x (float32, float16 or bfloat16) is quantised with
+    block_rows 1, w and w_scale come from fp8_quantize (mh3a_fp8_linear).  For channels-last frames
+    [B, T, C] pass x.view(B * T, C).  Returns [M, N] of x's type (``out`` if given)."""
+    what = "mh3a_fp8_linear"
+    M, K = _check_matrix(what, "x", x, DTYPES)
+    N, Kw, w_stride, w_rows = _check_stored(what, "w", w, w_scale)
+    if K != Kw:
+        raise _bad(what, f"x has {K} columns and w {Kw}", SHAPE)
+    if x.device != w.device:
+        raise _bad(what, "x and w are on different devices")
+    _check_bias_out(what, bias, out, x.device, (M, N), x.dtype)
+    L = _load()
+
+    def call(stream):
+        y = x.new_empty((M, N)) if out is None else out
+        n = L.mh3a_fp8_linear_workspace(M, K)
+        ws = x.new_empty(n, dtype=torch.uint8) if n else None
+        st = L.mh3a_fp8_linear(x.data_ptr(), DTYPES[x.dtype], _row_stride(x, K), w.data_ptr(), w_stride, w_scale.data_ptr(),
+                               w_rows, M, N, K, _ptr(bias), y.data_ptr(), _row_stride(y, N), _ptr(ws), n, stream)
+        if st:
+            _check(st, what)
+        return (y,)
+
+    return _launch(x.device, stream, call, (x, w, w_scale, bias, out))[0]

@@ -369,6 +369,52 @@ MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p, const void
                                                   float* dbias, float* dalpha, float* dbeta, void* workspace,
                                                   size_t workspace_bytes, void* stream);
 
+/* 8-bit floating point matrices (e4m3, largest value 448) with one fp32 scale for each block of 128
+ * values along the inner axis.  A matrix [rows, cols] is stored row by row, `stride` bytes apart, a
+ * multiple of 16; the base is 16-byte aligned; bytes between a row's end and the next row are never
+ * read.  With block_rows = 1 every row has scales of its own (activations, gradients); with
+ * block_rows = 128 a block spans 128 rows (weights).  Scales are fp32 [ceil(cols / 128)]
+ * [ceil(rows / block_rows)]: the rows of one inner block are adjacent.  Blocks at the ends are
+ * shorter.  A stored value q of a block with scale s stands for q s. */
+
+/* Quantise x (device, [rows, cols] of `dtype`, columns adjacent, rows x_stride >= 0 elements apart).
+ * Per block, in fp32: a = max(2^-100, the largest magnitude), s = a / 448, q = e4m3(x * (448 / a)),
+ * rounded to nearest, ties to even.  A NaN in a block makes the whole block and its scale NaN; an
+ * infinity makes its scale infinite.  With transpose = 1 the matrix that is stored and blocked is x
+ * transposed, [cols, rows]: the operands of the two gradient products.  q: device, q_stride bytes
+ * between its rows.  Errors: MH3A_ERR_INVALID_ARG (NULL or misaligned pointers, unknown dtype, a
+ * block_rows other than 1 or 128, a transpose other than 0 or 1, a negative x_stride, a q_stride
+ * below the row's length or not a multiple of 16), MH3A_ERR_SHAPE (rows or cols below 1 or above
+ * 2^30, or more than 2^30 blocks), MH3A_ERR_CUDA. */
+MH3A_API mh3a_status mh3a_fp8_quantize(const void* x, int dtype, int rows, int cols, long long x_stride,
+                                       int block_rows, int transpose, void* q, long long q_stride, float* scale,
+                                       void* stream);
+
+/* out[m, n] = sum_k a[m, k] b[n, k] + bias[n], a [M, K] with block_rows 1 and b [N, K] with
+ * b_block_rows 1 or 128, both as above.  The products of a block are added on the tensor cores, the
+ * blocks scaled and added in fp32; the sum is rounded once to out_dtype (mh3a_dtype).  bias: device
+ * fp32 [N] or NULL.  out: device, columns adjacent, rows out_stride elements apart; must not overlap
+ * an operand.  Errors: MH3A_ERR_INVALID_ARG (NULL or misaligned pointers, unknown dtype,
+ * b_block_rows other than 1 or 128, a stride below the row's length, an operand's stride not a
+ * multiple of 16 or 2^40 or more), MH3A_ERR_SHAPE (M, N or K below 1 or above 2^30, or more than
+ * 2^30 output tiles), MH3A_ERR_CUDA. */
+MH3A_API mh3a_status mh3a_fp8_matmul(const void* a, long long a_stride, const float* a_scale, const void* b,
+                                     long long b_stride, const float* b_scale, int b_block_rows, int M, int N, int K,
+                                     const float* bias, int out_dtype, void* out, long long out_stride, void* stream);
+
+/* y = x w^T + bias for activations x [M, K] of `dtype` (columns adjacent, rows x_stride >= 0 elements
+ * apart) and quantised weights w [N, K]: mh3a_fp8_quantize of x with block_rows 1, then
+ * mh3a_fp8_matmul with y of the same dtype.  Up to MH3A_FP8_FEW_ROWS rows it is one kernel that is
+ * bound by reading the weights, for a decode frame by frame.  `workspace`: device, 16-byte aligned,
+ * mh3a_fp8_linear_workspace bytes (0 for few rows; it may be NULL then).  Errors: as the two calls,
+ * and MH3A_ERR_INVALID_ARG for a workspace too small or misaligned. */
+#define MH3A_FP8_FEW_ROWS 8
+MH3A_API size_t mh3a_fp8_linear_workspace(int M, int K);
+MH3A_API mh3a_status mh3a_fp8_linear(const void* x, int dtype, long long x_stride, const void* w, long long w_stride,
+                                     const float* w_scale, int w_block_rows, int M, int N, int K, const float* bias,
+                                     void* y, long long y_stride, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 /* Release the handle's device memory.  NULL is ignored.  Waits for the handle's work. */
 MH3A_API void mh3a_destroy(mh3a_handle* h);
 

@@ -92,3 +92,35 @@ def norm_backward(dy, x, groups, weight, bias, act, alpha, beta, mean, rstd, len
         out["dx"][i, :n] = rs * (h - m1 - xh * m2)
         mag["dx"][i, :n] = rs * (p_h + a1 + xh.abs() * a2)
     return out, mag
+
+
+def e4m3(v):
+    """The e4m3 number nearest to each fp64 value (ties to even, at most 448 in magnitude; NaN stays)."""
+    e = torch.frexp(v.abs().clamp(min=2.0 ** -6).nan_to_num())[1].long() - 1
+    step = ((e - 3 + 1023) << 52).view(torch.float64)  # exactly a power of two
+    return torch.clamp(torch.round(v / step) * step, -448.0, 448.0)
+
+
+def quantize(x, block_rows):
+    """(q, scale [K blocks, row blocks], the values they stand for), fp64.  The scale and the number that is
+    rounded to e4m3 are fp32 by definition."""
+    R, K = x.shape
+    rb, kb = -(-R // block_rows), -(-K // 128)
+    p = torch.zeros(rb * block_rows, kb * 128, dtype=torch.float64, device=x.device)
+    p[:R, :K] = x.double()
+    p = p.view(rb, block_rows, kb, 128)
+    top = p.abs().amax(dim=(1, 3), keepdim=True).clamp(min=2.0 ** -100)
+    scale = (top / 448).float().double()
+    factor = (448 / top).float().double()
+    q = e4m3((p * factor).float().double())
+    v = (q * scale).view(rb * block_rows, kb * 128)[:R, :K]
+    return q.view(rb * block_rows, kb * 128)[:R, :K], scale[:, 0, :, 0].t(), v
+
+
+def dequantize(q, scale):
+    """The fp64 values of a stored matrix (block rows from the scale's shape)."""
+    R, K = q.shape
+    rows = 1 if scale.shape[1] == R else 128
+    at_r = torch.arange(R, device=q.device) // rows
+    at_k = torch.arange(K, device=q.device) // 128
+    return q.float().double() * scale.double()[at_k][:, at_r].t()
