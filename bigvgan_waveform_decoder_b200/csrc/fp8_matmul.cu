@@ -9,9 +9,11 @@
 // scaling costs no extra pass, and no accumulator in the tensor core sees more than one block.
 //
 // Warps: 0 loads tiles by TMA (128-byte swizzle, rows beyond the matrix and the short last block
-// filled with zeros), 1 issues the MMAs, 4.. are the epilogue (2 and 3 only fill up the warpgroup,
-// since a warp reads the quarter of tensor memory of its number modulo 4).  Persistent: a block takes
-// tiles blockIdx.x, + gridDim.x, ...
+// filled with zeros), 1 issues the MMAs, 2 copies column scales to shared memory a few steps ahead
+// where every column has its own, 4.. are the epilogue (3 only fills up the warpgroup, since a warp
+// reads the quarter of tensor memory of its number modulo 4).  The other scales are fetched into
+// registers steps ahead: a load that a step waits for costs more than the step.  Persistent: a
+// block takes tiles blockIdx.x, + gridDim.x, ...
 #include <cuda.h>
 
 #include <algorithm>
@@ -23,7 +25,10 @@ namespace mh3a {
 namespace fp8 {
 namespace {
 
-constexpr int kM = 128;  // tile rows (tensor-memory lanes)
+constexpr int kM = 128;     // tile rows (tensor-memory lanes)
+constexpr int kScaleSlots = 4;  // steps whose column scales are held or on their way
+constexpr int kAhead = 3;       // steps that row scales (and those of wide blocks) are fetched ahead
+constexpr int kPitch = 80;  // staging row of 64 bytes: 16-byte accesses of 8 rows meet no bank twice
 
 struct MatmulParams {
     const float* sa;    // [KB][M]
@@ -44,11 +49,18 @@ struct Cfg {
     static constexpr int kAcc = NT == 256 ? 2 : 4;        // tensor-memory buffers
     static constexpr int kCols = kAcc * NT < 32 ? 32 : kAcc * NT;
     static constexpr int kStageBytes = (kM + NT) * kBlock;
-    static constexpr int kPitch = 144;                    // staging row of 128 bytes, conflict-free
     static constexpr int kStaging = EW * 32 * kPitch;
-    static constexpr int kStages = std::min(8, (200 * 1024 - kStaging) / kStageBytes);
-    static constexpr int kSmem = kStages * kStageBytes + kStaging + 1024 + 256 + (CW * 4 * 2 * EW);
+    static constexpr int kOther = kStaging + kScaleSlots * NT * 4 + 1024 + 512;
+    static constexpr int kStages = std::min(8, (227 * 1024 - kOther) / kStageBytes);
+    static constexpr int kSmem = kStages * kStageBytes + kOther;
+    // 128 columns of sums and two buffers of 32 do not fit an even share of the registers
+    static constexpr bool kSplitRegs = CW == 128;
 };
+
+// The thread's earlier cp.async copies count as one arrival on the barrier once they are done.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+}
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
     asm volatile(
@@ -82,37 +94,39 @@ __device__ __forceinline__ void mma_block_elect(uint32_t d, uint64_t a, uint64_t
         : "memory");
 }
 
-// 32 lanes x 32 bits, W consecutive columns; the values are there after tmem_wait().
-template <int W>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[W]);
-template <>
-__device__ __forceinline__ void tmem_ld<16>(uint32_t addr, uint32_t (&r)[16]) {
+// 32 lanes x 32 bits, 16 consecutive columns; the values are there after tmem_wait().
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(addr));
 }
-template <>
-__device__ __forceinline__ void tmem_ld<32>(uint32_t addr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
+// Waits for every load before it; the values pass through, so that no use of them moves ahead.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
-__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+template <int W>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[W / 16][16]) {
+#pragma unroll
+    for (int i = 0; i < W / 16; ++i) tmem_ld(addr + 16 * i, r[i]);
+}
+template <int W>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[W / 16][16]) {
+#pragma unroll
+    for (int i = 0; i < W / 16; ++i) tmem_wait(r[i]);  // the second finds nothing left to wait for
+}
 
-// Writes a warp's 32 x CW results: 128 bytes of each row at a time go through shared memory, so that
-// global memory gets whole lines.
+// Writes a warp's 32 x CW results: 64 bytes of each row at a time go through shared memory, so that
+// global memory gets whole sectors.
 template <typename O, int CW>
 __device__ __forceinline__ void write_out(const MatmulParams& p, const float2 (&acc)[CW / 2], unsigned char* stage, int m0, int n0) {
-    constexpr int kPitch = 144;
-    constexpr int kStep = 128 / sizeof(O) < CW ? 128 / sizeof(O) : CW;  // columns at a time
-    constexpr int kVecs = kStep * sizeof(O) / 16;                       // 16-byte pieces of a row
+    constexpr int kStep = 64 / sizeof(O) < CW ? 64 / sizeof(O) : CW;  // columns at a time
+    constexpr int kVecs = kStep * sizeof(O) / 16;                     // 16-byte pieces of a row
     const int lane = threadIdx.x & 31;
     O* out = static_cast<O*>(p.out);
 #pragma unroll
@@ -127,10 +141,6 @@ __device__ __forceinline__ void write_out(const MatmulParams& p, const float2 (&
                 const int c = c0 + v * kPer + i;
                 f[i] = acc[c / 2].x;
                 f[i + 1] = acc[c / 2].y;
-                if (p.bias) {
-                    f[i] += n0 + c < p.N ? __ldg(p.bias + n0 + c) : 0.f;
-                    f[i + 1] += n0 + c + 1 < p.N ? __ldg(p.bias + n0 + c + 1) : 0.f;
-                }
             }
             uint4 q;
             if constexpr (sizeof(O) == 4) {
@@ -177,12 +187,14 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
     extern __shared__ unsigned char raw[];
     unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     unsigned char* staging = tiles + C::kStages * C::kStageBytes;
-    float* cols = reinterpret_cast<float*>(staging + C::kStaging);  // [EW][2][CW]: column scales
-    uint64_t* full = reinterpret_cast<uint64_t*>(cols + C::EW * 2 * C::CW);
+    float* scales = reinterpret_cast<float*>(staging + C::kStaging);  // [slot][NT]: column scales
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + kScaleSlots * NT);
     uint64_t* empty = full + C::kStages;
     uint64_t* done = empty + C::kStages;  // accumulator buffer filled
     uint64_t* freed = done + C::kAcc;     // and read again
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(freed + C::kAcc);
+    uint64_t* sfull = freed + C::kAcc;    // scales of a step are there
+    uint64_t* sempty = sfull + kScaleSlots;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + kScaleSlots);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0 && lane == 0) {
@@ -193,6 +205,10 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
         for (int i = 0; i < C::kAcc; ++i) {
             ptx::mbar_init(done + i, 1);
             ptx::mbar_init(freed + i, C::EW);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            ptx::mbar_init(sfull + i, 32);
+            ptx::mbar_init(sempty + i, C::EW);
         }
         ptx::fence_mbar_init();
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
@@ -209,8 +225,10 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
 
-    if (warp == 0) {
-        if (lane == 0) {
+    // Split registers: 128 x 80 + 256 x 208 of the 384 x 168 at launch.
+    if (warp < 4) {
+        if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 0 && lane == 0) {
             int it = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
@@ -225,93 +243,125 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                     tma_load_2d(to + kM * kBlock, &map_b, kb * kBlock, n0, full + s);
                 }
             }
-        }
-    } else if (warp == 1) {
-        constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);  // e4m3, fp32 sums
-        int it = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
-            for (int kb = 0; kb < p.KB; ++kb, ++it) {
-                const int s = it % C::kStages, b = it % C::kAcc;
-                if (it >= C::kAcc) ok = ptx::mbar_wait(freed + b, ((it / C::kAcc) & 1) ^ 1);
-                ok = ok && ptx::mbar_wait(full + s, (it / C::kStages) & 1);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint32_t at = ptx::smem_u32(tiles + s * C::kStageBytes);
-                mma_block_elect(tmem + b * NT, desc_sw128(at), desc_sw128(at + kM * kBlock), idesc);
-                ptx::mma_commit_elect(empty + s);
-                ptx::mma_commit_elect(done + b);
+        } else if (warp == 1) {
+            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);  // e4m3, fp32 sums
+            int it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+                for (int kb = 0; kb < p.KB; ++kb, ++it) {
+                    const int s = it % C::kStages, b = it % C::kAcc;
+                    if (it >= C::kAcc) ok = ptx::mbar_wait(freed + b, ((it / C::kAcc) & 1) ^ 1);
+                    ok = ok && ptx::mbar_wait(full + s, (it / C::kStages) & 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t at = ptx::smem_u32(tiles + s * C::kStageBytes);
+                    mma_block_elect(tmem + b * NT, desc_sw128(at), desc_sw128(at + kM * kBlock), idesc);
+                    ptx::mma_commit_elect(empty + s);
+                    ptx::mma_commit_elect(done + b);
+                }
+            }
+        } else if (warp == 2 && !WIDE) {
+            int it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+                const int n0 = (t / p.mt) * NT;
+                for (int kb = 0; kb < p.KB; ++kb, ++it) {
+                    const int s = it % kScaleSlots;
+                    if (it >= kScaleSlots) ok = ptx::mbar_wait(sempty + s, ((it / kScaleSlots) & 1) ^ 1);
+                    if (!ok) break;
+                    float* to = scales + s * NT;
+                    const float* sb = p.sb + (long long)kb * p.NB;
+#pragma unroll
+                    for (int i = 0; i < NT; i += 32)
+                        if (i + lane < NT) ptx::cp_async4(to + i + lane, sb + min(n0 + i + lane, p.NB - 1));
+                    cp_async_arrive(sfull + s);
+                }
             }
         }
-    } else if (warp >= 4) {
+    } else {
+        if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int e = warp - 4, quarter = warp & 3, half = e >> 2;
         const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::CW;
-        float* my_cols = cols + e * 2 * C::CW;
         int it = 0;
         for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
             const int m0 = (t % p.mt) * kM + quarter * 32, n0 = (t / p.mt) * NT + half * C::CW;
-            const int row = min(m0 + lane, p.M - 1);
             float2 acc[C::CW / 2];
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            // the scales of step 0; those of the next step are loaded while a step is added up
-            const int nb = min(n0, p.N - 1) / kBlock;
-            constexpr int kPer = (C::CW + 31) / 32;  // column scales a lane fetches
-            float sa = __ldg(p.sa + row), sb = 0.f, sc[kPer];
-            auto fetch_cols = [&](int kb) {
-                if constexpr (WIDE) {
-                    sb = __ldg(p.sb + (long long)kb * p.NB + nb);
-                } else {
+            if (p.bias) {  // lane l holds columns 32 j + l; a shuffle hands each to all rows
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        const int c = i * 32 + lane;
-                        sc[i] = __ldg(p.sb + (long long)kb * p.NB + min(n0 + c, p.N - 1));
-                    }
+                for (int j = 0; j < C::CW; j += 32) {
+                    const float v = __ldg(p.bias + min(n0 + j + lane, p.N - 1));
+#pragma unroll
+                    for (int i = 0; i < (C::CW < 32 ? C::CW : 32); i += 2)
+                        acc[(j + i) / 2] = make_float2(__shfl_sync(0xffffffffu, v, i), __shfl_sync(0xffffffffu, v, i + 1));
                 }
-            };
-            fetch_cols(0);
+            }
+            const float* psa = p.sa + min(m0 + lane, p.M - 1);
+            const float* psb = p.sb + min(n0 / kBlock, p.NB - 1);
+            float sa[kAhead], sb[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                sa[i] = i < p.KB ? __ldg(psa + (long long)i * p.M) : 0.f;
+                sb[i] = WIDE && i < p.KB ? __ldg(psb + (long long)i * p.NB) : 1.f;
+            }
             bool ok = true;
             for (int kb = 0; kb < p.KB; ++kb, ++it) {
-                const int b = it % C::kAcc;
-                float* now = my_cols + (kb & 1) * C::CW;
-                const float s1 = WIDE ? sa * sb : sa;
-                if constexpr (!WIDE) {
+                const int b = it % C::kAcc, s = it % kScaleSlots;
+                const float* now = scales + s * NT + half * C::CW;
+                const float s1 = WIDE ? sa[0] * sb[0] : sa[0];
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i)
-                        if (i * 32 + lane < C::CW) now[i * 32 + lane] = sc[i];
-                    __syncwarp();
+                for (int i = 0; i + 1 < kAhead; ++i) {
+                    sa[i] = sa[i + 1];
+                    sb[i] = sb[i + 1];
                 }
-                if (kb + 1 < p.KB) {
-                    sa = __ldg(p.sa + (long long)(kb + 1) * p.M + row);
-                    fetch_cols(kb + 1);
+                if (kb + kAhead < p.KB) {
+                    sa[kAhead - 1] = __ldg(psa + (long long)(kb + kAhead) * p.M);
+                    if (WIDE) sb[kAhead - 1] = __ldg(psb + (long long)(kb + kAhead) * p.NB);
                 }
+                if (!WIDE) ok = ok && ptx::mbar_wait(sfull + s, (it / kScaleSlots) & 1);
                 ok = ok && ptx::mbar_wait(done + b, (it / C::kAcc) & 1);
                 ptx::tc_fence_after();
                 const float2 s2 = make_float2(s1, s1);
-                constexpr int kLd = C::CW >= 32 ? 32 : 16;
+                // the next columns are on their way while a piece is added up
+                constexpr int kLd = C::CW >= 32 ? 32 : 16, kPieces = C::CW / kLd;
+                uint32_t v[2][kLd / 16][16];
+                tmem_ld<kLd>(mine + b * NT, v[0]);
 #pragma unroll
-                for (int c = 0; c < C::CW; c += kLd) {
-                    uint32_t v[kLd];
-                    tmem_ld<kLd>(mine + b * NT + c, v);
-                    tmem_wait();
-                    if (c + kLd == C::CW) {  // the buffer is read: the tensor core may fill it again
+                for (int c = 0; c < kPieces; ++c) {
+                    tmem_wait<kLd>(v[c & 1]);
+                    if (c + 1 < kPieces) {
+                        tmem_ld<kLd>(mine + b * NT + (c + 1) * kLd, v[(c + 1) & 1]);
+                    } else {  // the buffer is read: the tensor core may fill it again
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(freed + b);
                     }
 #pragma unroll
-                    for (int i = 0; i < kLd / 2; ++i) {
-                        float2 f = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                        if constexpr (!WIDE) f = __fmul2_rn(f, *reinterpret_cast<const float2*>(now + c + 2 * i));
-                        acc[c / 2 + i] = __ffma2_rn(f, s2, acc[c / 2 + i]);
+                    for (int i = 0; i < kLd / 4; ++i) {
+                        const uint32_t* w = &v[c & 1][i / 4][4 * (i % 4)];
+                        float2 f = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+                        float2 h = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+                        if constexpr (!WIDE) {
+                            const float4 q = *reinterpret_cast<const float4*>(now + c * kLd + 4 * i);
+                            f = __fmul2_rn(f, make_float2(q.x, q.y));
+                            h = __fmul2_rn(h, make_float2(q.z, q.w));
+                        }
+                        float2* to = acc + (c * kLd + 4 * i) / 2;
+                        to[0] = __ffma2_rn(f, s2, to[0]);
+                        to[1] = __ffma2_rn(h, s2, to[1]);
                     }
+                }
+                if (!WIDE) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(sempty + s);
                 }
             }
             if (!ok) {  // never expected: a wait ran out of time; NaN rather than a partial sum
 #pragma unroll
                 for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
             }
-            write_out<O, C::CW>(p, acc, staging + e * 32 * C::kPitch, m0, n0);
+            write_out<O, C::CW>(p, acc, staging + e * 32 * kPitch, m0, n0);
         }
     }
     ptx::tc_fence_before();
