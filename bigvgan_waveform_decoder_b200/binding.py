@@ -64,6 +64,12 @@ class mh3a_tensor(C.Structure):
     ]
 
 
+class mh3a_norm(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("act", C.c_int), ("B", C.c_int), ("T", C.c_int), ("C", C.c_int),
+                ("groups", C.c_int), ("eps", C.c_float), ("weight", C.c_void_p), ("bias", C.c_void_p),
+                ("alpha", C.c_void_p), ("beta", C.c_void_p), ("lengths", C.c_void_p)]
+
+
 ALLOC_FN = C.CFUNCTYPE(C.c_void_p, C.c_size_t, C.c_void_p)
 RELEASE_FN = C.CFUNCTYPE(None, C.c_void_p, C.c_void_p)
 
@@ -139,6 +145,22 @@ def load():
     L.mh3a_status_string.restype = C.c_char_p
     L.mh3a_last_error.argtypes = []
     L.mh3a_last_error.restype = C.c_char_p
+    ll, i, sz = C.c_longlong, C.c_int, C.c_size_t
+    norm = C.POINTER(mh3a_norm)
+    L.mh3a_group_norm_act_workspace.argtypes = [norm, i]
+    L.mh3a_group_norm_act_workspace.restype = sz
+    L.mh3a_group_norm_act.argtypes = [norm, vp, ll, ll, vp, vp, vp, vp, sz, vp]
+    L.mh3a_group_norm_act.restype = i
+    L.mh3a_group_norm_act_backward.argtypes = [norm, vp, ll, ll, vp, ll, ll, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.mh3a_group_norm_act_backward.restype = i
+    L.mh3a_fp8_quantize.argtypes = [vp, i, i, i, ll, i, i, vp, ll, vp, vp]
+    L.mh3a_fp8_quantize.restype = i
+    L.mh3a_fp8_matmul.argtypes = [vp, ll, vp, vp, ll, vp, i, i, i, i, vp, i, vp, ll, vp]
+    L.mh3a_fp8_matmul.restype = i
+    L.mh3a_fp8_linear_workspace.argtypes = [i, i]
+    L.mh3a_fp8_linear_workspace.restype = sz
+    L.mh3a_fp8_linear.argtypes = [vp, i, ll, vp, ll, vp, i, i, i, i, vp, vp, ll, vp, sz, vp]
+    L.mh3a_fp8_linear.restype = i
     _lib = L
     return L
 

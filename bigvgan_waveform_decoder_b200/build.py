@@ -3,7 +3,8 @@
     python -m bigvgan_waveform_decoder_b200.build     # writes bigvgan_waveform_decoder_b200/libmh3a.so
 
 nvcc compiles every csrc/*.cu for sm_100a and links one shared library exporting the C ABI of
-include/mh3a.h.  No GPU is needed to build.
+include/mh3a.h.  It then builds _ops.so, the operators' front end for torch tensors, on that library
+and the installed torch.  No GPU is needed to build.
 """
 from __future__ import annotations
 
@@ -16,6 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmh3a.so")
+OPS_SRC = os.path.join(CSRC, "torch_ops.cpp")
+OPS = os.path.join(HERE, "_ops.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -35,14 +38,51 @@ def _deps():
         os.path.join(ROOT, "include", "mh3a.h"), os.path.abspath(__file__)]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(out, deps) -> bool:
+    if not os.path.exists(out):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _deps())
 
 
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
+    build_library(force, verbose, extra)
+    build_ops(force, verbose)
+    return LIB
+
+
+def build_ops(force: bool = False, verbose: bool = False) -> str:
+    """_ops.so: csrc/torch_ops.cpp against libmh3a.so and torch."""
+    header = os.path.join(ROOT, "include", "mh3a.h")
+    if not force and _newer(OPS, [OPS_SRC, header, os.path.abspath(__file__)]):
+        return OPS
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    inc = [*include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = OPS + f".tmp{os.getpid()}"
+    # nvcc hands the file to its host compiler and links the C++ library dynamically, as for libmh3a.so:
+    # a copy of its own inside _ops.so would not get along with torch's
+    cmd = [NVCC, *FLAGS[:2], "-shared", "-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_ops",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *[f for i in inc for f in ("-isystem", i)],
+           OPS_SRC, "-o", tmp, "-L", HERE, "-l:libmh3a.so", "-Xlinker", "-rpath=$ORIGIN", "-L", lib, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "--cudart", "none"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, OPS)
+    return OPS
+
+
+def build_library(force: bool = False, verbose: bool = False, extra=None) -> str:
     if not force and up_to_date():
         return LIB
     objdir = os.path.join(HERE, "_build")

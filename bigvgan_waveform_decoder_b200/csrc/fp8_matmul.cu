@@ -421,7 +421,7 @@ int launch(const MatmulArgs& m, cudaStream_t s) {
     CUtensorMap ma, mb;
     if (!make_map(&ma, m.a, m.M, m.K, m.as, kM) || !make_map(&mb, m.b, m.N, m.K, m.bs, NT)) return -1;
     auto kern = k_fp8_matmul<O, NT, WIDE>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return -1;
+    if (!allow_smem<k_fp8_matmul<O, NT, WIDE>>(C::kSmem)) return -1;
     const int grid = std::min(p.tiles, kSms);
     return launch_dependent(kern, dim3(grid), dim3(C::kThreads), C::kSmem, s, p, ma, mb) == cudaSuccess ? 1 : -1;
 }

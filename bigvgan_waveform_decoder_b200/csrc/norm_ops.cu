@@ -598,10 +598,9 @@ bool plan_resident(const NormArgs& a, int V, int e, int bytes_row, Extra extra, 
     return false;
 }
 
-template <typename K, typename... Args>
-bool go_resident(K kern, const NormArgs& a, const Resident& r, cudaStream_t s, Args... args) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kResOne) != cudaSuccess) return false;
-    if (r.S > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+template <auto Kern>
+bool go_resident(const NormArgs& a, const Resident& r, cudaStream_t s) {
+    if (!allow_smem<Kern>(kResOne, true)) return false;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(r.S, r.slabs, a.B);
     cfg.blockDim = dim3(kResThreads);
@@ -615,13 +614,13 @@ bool go_resident(K kern, const NormArgs& a, const Resident& r, cudaStream_t s, A
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, a, r, args...) == cudaSuccess;
+    return cudaLaunchKernelEx(&cfg, Kern, a, r) == cudaSuccess;
 }
 
 template <typename T, int V, int ACT>
 bool forward_resident(const NormArgs& a, const Resident& r, cudaStream_t s) {
-    return a.D % V == 0 ? go_resident(k_norm_resident<T, V, ACT, true>, a, r, s)
-                        : go_resident(k_norm_resident<T, V, ACT, false>, a, r, s);
+    return a.D % V == 0 ? go_resident<k_norm_resident<T, V, ACT, true>>(a, r, s)
+                        : go_resident<k_norm_resident<T, V, ACT, false>>(a, r, s);
 }
 
 template <typename T, int V>
@@ -672,8 +671,8 @@ bool backward_act(NormArgs& a, bool vec, cudaStream_t s) {
     Resident r;
     auto extra = [&](int W, int S) { return res_bwd_extra(W, a.D, V, S, NS); };
     if (vec && plan_resident(a, V, sizeof(T), 2 * sizeof(T), extra, &r)) {
-        const bool ok = a.D % V == 0 ? go_resident(k_norm_bwd_resident<T, V, ACT, true>, a, r, s)
-                                     : go_resident(k_norm_bwd_resident<T, V, ACT, false>, a, r, s);
+        const bool ok = a.D % V == 0 ? go_resident<k_norm_bwd_resident<T, V, ACT, true>>(a, r, s)
+                                     : go_resident<k_norm_bwd_resident<T, V, ACT, false>>(a, r, s);
         if (!ok || a.B == 1) return ok;
         return go(k_norm_bwd_final, (a.C + 255LL) / 256, 256, s, a, (const float*)a.ws, (float2*)nullptr, NS, 0);
     }

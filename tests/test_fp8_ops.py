@@ -6,7 +6,6 @@ import torch
 
 import bigvgan_waveform_decoder_b200 as pkg
 from bigvgan_waveform_decoder_b200 import binding as Bd
-from bigvgan_waveform_decoder_b200 import ops
 
 from . import ops_ref as R
 
@@ -107,7 +106,7 @@ def test_quantize_strided(mode):
 @pytest.mark.gpu
 def test_quantize_writes_nothing_behind_its_rows():
     """Through the ABI with guard bytes: between the rows, and behind the last one."""
-    L = ops._load()
+    L = Bd.load()
     x = rand(37, 141, seed=5)
     for transpose in (0, 1):
         outer, inner = (141, 37) if transpose else (37, 141)
@@ -344,7 +343,7 @@ def test_python_refusals():
 
 def test_abi_refusals():
     """Every refusal comes before any device work (the pointers here are no device memory)."""
-    L, ok = ops._load(), 1 << 20
+    L, ok = Bd.load(), 1 << 20
 
     def quant(x=ok, dtype=0, rows=10, cols=256, xs=256, br=1, tr=0, q=ok, qs=256, scale=ok):
         return L.mh3a_fp8_quantize(x, dtype, rows, cols, xs, br, tr, q, qs, scale, None)
@@ -379,4 +378,4 @@ def test_abi_refusals():
 
 def test_exports():
     assert {"mh3a_fp8_quantize", "mh3a_fp8_matmul", "mh3a_fp8_linear", "mh3a_fp8_linear_workspace"} <= set(Bd.EXPORTS)
-    assert C.sizeof(ops.mh3a_norm) == 72
+    assert C.sizeof(Bd.mh3a_norm) == 72

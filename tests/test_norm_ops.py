@@ -6,7 +6,6 @@ import torch
 
 import bigvgan_waveform_decoder_b200 as pkg
 from bigvgan_waveform_decoder_b200 import binding as Bd
-from bigvgan_waveform_decoder_b200 import ops
 
 from . import ops_ref as R
 
@@ -288,7 +287,7 @@ def test_python_refusals():
 
 
 def norm(**kw):
-    p = ops.mh3a_norm(1, 1, 2, 10, 24, 3, 1e-5, None, None, None, None, None)
+    p = Bd.mh3a_norm(1, 1, 2, 10, 24, 3, 1e-5, None, None, None, None, None)
     for k, v in kw.items():
         setattr(p, k, v)
     return p
@@ -296,7 +295,7 @@ def norm(**kw):
 
 def test_abi_refusals():
     """Every refusal comes before any device work (the pointers here are no device memory)."""
-    L = ops._load()
+    L = Bd.load()
     p0, ok = C.byref(norm()), 1 << 20
     size = L.mh3a_group_norm_act_workspace(p0, 0)
     assert size > 0 and L.mh3a_group_norm_act_workspace(p0, 1) >= size
@@ -327,6 +326,15 @@ def test_abi_refusals():
         assert bwd(good, **kw) == 1, kw
     assert bwd(norm(groups=7)) == 3
     assert L.mh3a_group_norm_act_workspace(None, 0) == 0
+
+
+def test_tensors_that_are_not_on_a_gpu_are_refused():
+    x = torch.zeros(1, 2, 4)
+    for bad in (lambda: pkg.group_norm_act(x, 2), lambda: pkg.group_norm_act_backward(x, x, x[0, :, :2], x[0, :, :2], 2),
+                lambda: pkg.fp8_quantize(x[0]), lambda: pkg.fp8_linear(x[0], x[0], x[0]), lambda: pkg.fp8_matmul(x[0], x[0], x[0], x[0])):
+        with pytest.raises(pkg.MH3AError, match="not a CUDA tensor") as e:
+            bad()
+        assert e.value.status == 1
 
 
 def test_exports():
