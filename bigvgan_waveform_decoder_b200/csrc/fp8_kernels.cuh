@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "mh3a_internal.cuh"
 #include "ops_common.cuh"
 #include "tc_ptx.cuh"
@@ -32,6 +34,13 @@ __device__ __forceinline__ float as_float<__half>(__half v) { return __half2floa
 template <>
 __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+// Two 16-bit values, the first in the low half.
+template <typename T>
+__device__ __forceinline__ float2 pair(uint32_t w) {
+    if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
 // Four consecutive elements; `vec`: they all exist and are aligned to their size, else the `n` that
 // exist are read one by one and the others are 0.
 template <typename T>
@@ -41,9 +50,9 @@ __device__ __forceinline__ float4 load4(const T* p, bool vec, int n) {
         if constexpr (sizeof(T) == 4) {
             v = *reinterpret_cast<const float4*>(p);
         } else {
-            struct alignas(8) Q { T e[4]; };
-            const Q q = *reinterpret_cast<const Q*>(p);
-            v = make_float4(as_float<T>(q.e[0]), as_float<T>(q.e[1]), as_float<T>(q.e[2]), as_float<T>(q.e[3]));
+            const uint2 q = *reinterpret_cast<const uint2*>(p);
+            const float2 lo = pair<T>(q.x), hi = pair<T>(q.y);
+            v = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
     } else {
         if (n > 0) v.x = as_float<T>(p[0]);
@@ -72,6 +81,7 @@ struct QuantArgs {
     float* scale;
     int rows, cols;
     int vec;       // four adjacent elements of x can be read at once
+    int vec16;     // rows of 16-bit x start on 16-byte boundaries, rows of q on 8-byte ones
 };
 
 // Launchers: number of kernels, or -1.

@@ -202,8 +202,9 @@ extern "C" MH3A_API mh3a_status mh3a_fp8_quantize(const void* x, int dtype, int 
     if (!aligned(x, elem(dtype)) || !aligned(scale, 4) || !stored_ok(q, qs, transpose ? rows : cols)) return MH3A_ERR_INVALID_ARG;
     const long long grid = block_rows == 1 && !transpose ? blocks(cols) * ((rows + 31LL) / 32) : blocks(cols) * blocks(rows);
     if (grid > kMostSize) return MH3A_ERR_SHAPE;
-    QuantArgs a{x, x_stride, static_cast<unsigned char*>(q), qs, scale, rows, cols, 0};
+    QuantArgs a{x, x_stride, static_cast<unsigned char*>(q), qs, scale, rows, cols, 0, 0};
     a.vec = aligned(x, 4 * elem(dtype)) && x_stride % 4 == 0;
+    a.vec16 = elem(dtype) == 2 && aligned(x, 16) && x_stride % 8 == 0;
     return launch_quantize(a, dtype, block_rows, transpose, static_cast<cudaStream_t>(stream)) < 0 ? launch_failed("mh3a_fp8_quantize")
                                                                                                    : MH3A_OK;
 }
