@@ -121,44 +121,72 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[W / 16][16]) {
     for (int i = 0; i < W / 16; ++i) tmem_wait(r[i]);  // the second finds nothing left to wait for
 }
 
+// 16 lanes x 256 bits, W consecutive columns of 8: lane t gets, for columns 8 i + 2 (t % 4) + {0, 1}, row
+// t / 4 in r[4 i], r[4 i + 1] and row t / 4 + 8 in r[4 i + 2], r[4 i + 3].
+__device__ __forceinline__ void tmem_ld_frag(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_frag(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+
+// Two neighbouring results as they are stored.
+template <typename O>
+struct Out2 {
+    using Raw = typename std::conditional<sizeof(O) == 4, uint2, uint32_t>::type;
+    static __device__ __forceinline__ Raw pack(float2 f) {
+        if constexpr (sizeof(O) == 4) {
+            return make_uint2(__float_as_uint(f.x), __float_as_uint(f.y));
+        } else if constexpr (std::is_same<O, __half>::value) {
+            const __half2 h = __floats2half2_rn(f.x, f.y);
+            return *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+            return *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+};
+
 // Writes a warp's 32 x CW results: 64 bytes of each row at a time go through shared memory, so that
 // global memory gets whole sectors.
-template <typename O, int CW>
+// FRAG: the sums lie as tmem_ld_frag leaves them, acc[4 i + r / 8] for row t / 4 + r; else acc[c / 2] of row t.
+template <typename O, int CW, bool FRAG>
 __device__ __forceinline__ void write_out(const MatmulParams& p, const float2 (&acc)[CW / 2], unsigned char* stage, int m0, int n0) {
     constexpr int kStep = 64 / sizeof(O) < CW ? 64 / sizeof(O) : CW;  // columns at a time
     constexpr int kVecs = kStep * sizeof(O) / 16;                     // 16-byte pieces of a row
+    using Raw = typename Out2<O>::Raw;
     const int lane = threadIdx.x & 31;
     O* out = static_cast<O*>(p.out);
 #pragma unroll
     for (int c0 = 0; c0 < CW; c0 += kStep) {
-        unsigned char* to = stage + lane * kPitch;
+        if constexpr (FRAG) {
+            unsigned char* to = stage + (lane >> 2) * kPitch + (lane & 3) * sizeof(Raw);
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-            constexpr int kPer = 16 / sizeof(O);
-            float f[kPer];
+            for (int i = 0; i < kStep / 8; ++i)
 #pragma unroll
-            for (int i = 0; i < kPer; i += 2) {
-                const int c = c0 + v * kPer + i;
-                f[i] = acc[c / 2].x;
-                f[i + 1] = acc[c / 2].y;
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<Raw*>(to + r * 8 * kPitch + i * 4 * sizeof(Raw)) = Out2<O>::pack(acc[(c0 / 8 + i) * 4 + r]);
+        } else {
+            unsigned char* to = stage + lane * kPitch;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                Raw q[16 / sizeof(Raw)];
+#pragma unroll
+                for (int i = 0; i < (int)(16 / sizeof(Raw)); ++i) q[i] = Out2<O>::pack(acc[c0 / 2 + v * (16 / sizeof(Raw)) + i]);
+                *reinterpret_cast<uint4*>(to + v * 16) = *reinterpret_cast<const uint4*>(q);
             }
-            uint4 q;
-            if constexpr (sizeof(O) == 4) {
-                q = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-            } else {
-                uint32_t* w = &q.x;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (std::is_same<O, __half>::value) {
-                        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-                        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                    } else {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                }
-            }
-            *reinterpret_cast<uint4*>(to + v * 16) = q;
         }
         __syncwarp();
 #pragma unroll
@@ -203,7 +231,7 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
             ptx::mbar_init(empty + i, 1);
         }
         for (int i = 0; i < C::kAcc; ++i) {
-            ptx::mbar_init(done + i, 1);
+            ptx::mbar_init(done + i, WIDE ? 1 : 2);  // the MMAs; and the step's column scales
             ptx::mbar_init(freed + i, C::EW);
         }
         for (int i = 0; i < kScaleSlots; ++i) {
@@ -248,7 +276,7 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
             int it = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
-                for (int kb = 0; kb < p.KB; ++kb, ++it) {
+                for (int kb = 0; kb < p.KB && ok; ++kb, ++it) {
                     const int s = it % C::kStages, b = it % C::kAcc;
                     if (it >= C::kAcc) ok = ptx::mbar_wait(freed + b, ((it / C::kAcc) & 1) ^ 1);
                     ok = ok && ptx::mbar_wait(full + s, (it / C::kStages) & 1);
@@ -258,6 +286,10 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                     mma_block_elect(tmem + b * NT, desc_sw128(at), desc_sw128(at + kM * kBlock), idesc);
                     ptx::mma_commit_elect(empty + s);
                     ptx::mma_commit_elect(done + b);
+                    if (!WIDE) {
+                        ok = ptx::mbar_wait(sfull + it % kScaleSlots, (it / kScaleSlots) & 1);
+                        if (lane == 0) ptx::mbar_arrive(done + b);
+                    }
                 }
             }
         } else if (warp == 2 && !WIDE) {
@@ -288,68 +320,110 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
             float2 acc[C::CW / 2];
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            if (p.bias) {  // lane l holds columns 32 j + l; a shuffle hands each to all rows
+            if (p.bias) {
+                if constexpr (WIDE) {  // lane l holds columns 32 j + l; a shuffle hands each to all rows
 #pragma unroll
-                for (int j = 0; j < C::CW; j += 32) {
-                    const float v = __ldg(p.bias + min(n0 + j + lane, p.N - 1));
+                    for (int j = 0; j < C::CW; j += 32) {
+                        const float v = __ldg(p.bias + min(n0 + j + lane, p.N - 1));
 #pragma unroll
-                    for (int i = 0; i < (C::CW < 32 ? C::CW : 32); i += 2)
-                        acc[(j + i) / 2] = make_float2(__shfl_sync(0xffffffffu, v, i), __shfl_sync(0xffffffffu, v, i + 1));
+                        for (int i = 0; i < (C::CW < 32 ? C::CW : 32); i += 2)
+                            acc[(j + i) / 2] = make_float2(__shfl_sync(0xffffffffu, v, i), __shfl_sync(0xffffffffu, v, i + 1));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C::CW / 8; ++i) {
+                        const int n = n0 + 8 * i + 2 * (lane & 3);
+                        const float2 v = make_float2(__ldg(p.bias + min(n, p.N - 1)), __ldg(p.bias + min(n + 1, p.N - 1)));
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[4 * i + r] = v;
+                    }
                 }
             }
-            const float* psa = p.sa + min(m0 + lane, p.M - 1);
+            // scales of rows: its own (WIDE), or the four of the fragments
+            constexpr int kRows = WIDE ? 1 : 4;
+            const float* psa[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) psa[r] = p.sa + min(m0 + (WIDE ? lane : (lane >> 2) + 8 * r), p.M - 1);
             const float* psb = p.sb + min(n0 / kBlock, p.NB - 1);
-            float sa[kAhead], sb[kAhead];
+            float sa[kAhead][kRows], sb[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                sa[i] = i < p.KB ? __ldg(psa + (long long)i * p.M) : 0.f;
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) sa[i][r] = i < p.KB ? __ldg(psa[r] + (long long)i * p.M) : 0.f;
                 sb[i] = WIDE && i < p.KB ? __ldg(psb + (long long)i * p.NB) : 1.f;
             }
             bool ok = true;
             for (int kb = 0; kb < p.KB; ++kb, ++it) {
                 const int b = it % C::kAcc, s = it % kScaleSlots;
                 const float* now = scales + s * NT + half * C::CW;
-                const float s1 = WIDE ? sa[0] * sb[0] : sa[0];
+                float s1[kRows];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) s1[r] = sa[0][r] * sb[0];
 #pragma unroll
                 for (int i = 0; i + 1 < kAhead; ++i) {
-                    sa[i] = sa[i + 1];
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) sa[i][r] = sa[i + 1][r];
                     sb[i] = sb[i + 1];
                 }
                 if (kb + kAhead < p.KB) {
-                    sa[kAhead - 1] = __ldg(psa + (long long)(kb + kAhead) * p.M);
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) sa[kAhead - 1][r] = __ldg(psa[r] + (long long)(kb + kAhead) * p.M);
                     if (WIDE) sb[kAhead - 1] = __ldg(psb + (long long)(kb + kAhead) * p.NB);
                 }
-                if (!WIDE) ok = ok && ptx::mbar_wait(sfull + s, (it / kScaleSlots) & 1);
                 ok = ok && ptx::mbar_wait(done + b, (it / C::kAcc) & 1);
                 ptx::tc_fence_after();
-                const float2 s2 = make_float2(s1, s1);
                 // the next columns are on their way while a piece is added up
                 constexpr int kLd = C::CW >= 32 ? 32 : 16, kPieces = C::CW / kLd;
-                uint32_t v[2][kLd / 16][16];
-                tmem_ld<kLd>(mine + b * NT, v[0]);
+                const uint32_t buf = mine + b * NT;
+                auto hand_back = [&]() {  // the buffer is read: the tensor core may fill it again
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(freed + b);
+                };
+                if constexpr (WIDE) {
+                    const float2 s2 = make_float2(s1[0], s1[0]);
+                    uint32_t v[2][kLd / 16][16];
+                    tmem_ld<kLd>(buf, v[0]);
 #pragma unroll
-                for (int c = 0; c < kPieces; ++c) {
-                    tmem_wait<kLd>(v[c & 1]);
-                    if (c + 1 < kPieces) {
-                        tmem_ld<kLd>(mine + b * NT + (c + 1) * kLd, v[(c + 1) & 1]);
-                    } else {  // the buffer is read: the tensor core may fill it again
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(freed + b);
-                    }
+                    for (int c = 0; c < kPieces; ++c) {
+                        tmem_wait<kLd>(v[c & 1]);
+                        if (c + 1 < kPieces) tmem_ld<kLd>(buf + (c + 1) * kLd, v[(c + 1) & 1]);
+                        else hand_back();
 #pragma unroll
-                    for (int i = 0; i < kLd / 4; ++i) {
-                        const uint32_t* w = &v[c & 1][i / 4][4 * (i % 4)];
-                        float2 f = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
-                        float2 h = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
-                        if constexpr (!WIDE) {
-                            const float4 q = *reinterpret_cast<const float4*>(now + c * kLd + 4 * i);
-                            f = __fmul2_rn(f, make_float2(q.x, q.y));
-                            h = __fmul2_rn(h, make_float2(q.z, q.w));
+                        for (int i = 0; i < kLd / 2; ++i) {
+                            const uint32_t* w = &v[c & 1][i / 8][2 * (i % 8)];
+                            float2& to = acc[c * kLd / 2 + i];
+                            to = __ffma2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), s2, to);
                         }
-                        float2* to = acc + (c * kLd + 4 * i) / 2;
-                        to[0] = __ffma2_rn(f, s2, to[0]);
-                        to[1] = __ffma2_rn(h, s2, to[1]);
+                    }
+                } else {
+                    // Column scales: a lane of the fragments needs a quarter of them, where a lane that holds a
+                    // whole row would read all from shared memory, 512 bytes a load and four columns (74 us
+                    // against 66 at 2048 x 2048 x 6400).
+                    uint32_t v[2][2][kLd / 2];
+                    auto load = [&](int c) {
+                        tmem_ld_frag(buf + c * kLd, v[c & 1][0]);
+                        tmem_ld_frag(buf + c * kLd + (16u << 16), v[c & 1][1]);
+                    };
+                    const float* cs = now + 2 * (lane & 3);
+                    load(0);
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c) {
+                        tmem_wait(v[c & 1][0]);
+                        tmem_wait(v[c & 1][1]);
+                        if (c + 1 < kPieces) load(c + 1);
+                        else hand_back();
+#pragma unroll
+                        for (int i = 0; i < kLd / 8; ++i) {
+                            const float2 k2 = *reinterpret_cast<const float2*>(cs + c * kLd + 8 * i);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const uint32_t* w = &v[c & 1][r / 2][4 * i + 2 * (r % 2)];
+                                const float2 f = __fmul2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), k2);
+                                float2& to = acc[(c * kLd / 8 + i) * 4 + r];
+                                to = __ffma2_rn(f, make_float2(s1[r], s1[r]), to);
+                            }
+                        }
                     }
                 }
                 if (!WIDE) {
@@ -361,7 +435,7 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
 #pragma unroll
                 for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
             }
-            write_out<O, C::CW>(p, acc, staging + e * 32 * kPitch, m0, n0);
+            write_out<O, C::CW, !WIDE>(p, acc, staging + e * 32 * kPitch, m0, n0);
         }
     }
     ptx::tc_fence_before();
