@@ -22,7 +22,6 @@ namespace mh3a {
 namespace norm {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // rows a thread has in flight
 
 // One block's place: item b, channel tile, row chunk.
 struct Place {
@@ -45,6 +44,87 @@ __device__ __forceinline__ Place place(const NormArgs& a, unsigned id) {
     p.c = p.live ? (int)c : 0;
     return p;
 }
+
+// A thread's rows of N tensors, streamed through shared memory: kRing rows, in pairs, are on their way while
+// one is worked on, with no registers held.  Only the thread itself reads its slots, so no barrier is needed.
+// Element types that cp.async cannot copy (2 bytes) are loaded where they are used.
+template <typename T, int V, int N>
+struct Stream {
+    static constexpr int kBytes = sizeof(T) * V;
+    static constexpr bool kAsync = kBytes >= 4;
+    static constexpr int kRing = kBytes * N > 16 ? 4 : 8;  // 32 KB a block at most
+    static constexpr size_t kSmem = kAsync ? (size_t)kRing * N * kThreads * kBytes : 16;
+    const T* at[N];
+    long long step[N];
+    Pack<T, V>* slots;
+    int mine, issued, taken;
+
+    __device__ __forceinline__ void fetch_pair() {
+#pragma unroll
+        for (int j = 0; j < 2; ++j, ++issued) {
+            if (issued < mine) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const uint32_t to = ptx::smem_u32(slots + ((issued & (kRing - 1)) * N + i) * kThreads);
+                    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(at[i]) : "memory");
+                    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(at[i]), "n"(kBytes < 4 ? 4 : kBytes) : "memory");
+                    at[i] += step[i];
+                }
+            }
+        }
+        ptx::cp_async_commit();
+    }
+    __device__ __forceinline__ void start(void* smem, int rows) {
+        slots = static_cast<Pack<T, V>*>(smem) + threadIdx.x;
+        mine = rows;
+        issued = taken = 0;
+        if constexpr (kAsync) {
+#pragma unroll
+            for (int k = 0; k < kRing / 2; ++k) fetch_pair();
+        }
+    }
+    // Calls f(rows of the N tensors) for every row in turn.
+    template <typename F>
+    __device__ __forceinline__ void run(F f) {
+        if constexpr (kAsync) {
+            for (; taken < mine; taken += 2) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRing / 2 - 1) : "memory");
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (taken + j < mine) {
+                        Pack<T, V> r[N];
+#pragma unroll
+                        for (int i = 0; i < N; ++i) r[i] = slots[(((taken + j) & (kRing - 1)) * N + i) * kThreads];
+                        f(r);
+                    }
+                }
+                fetch_pair();
+            }
+            ptx::cp_async_wait_all();
+        } else {
+            for (; taken < mine; ++taken) {
+                Pack<T, V> r[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    r[i] = load_pack<T, V>(at[i]);
+                    at[i] += step[i];
+                }
+                f(r);
+            }
+        }
+    }
+    // The sum of the first rows (up to four), which stay to be run over: f(row) for each; their number.
+    template <typename F>
+    __device__ __forceinline__ int peek(F f) {
+        const int n = min(mine, 4);
+        if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kRing / 2 - 2) : "memory");
+        for (int k = 0; k < n; ++k) {
+            if constexpr (kAsync) f(slots[k * N * kThreads]);
+            else f(load_pack<T, V>(at[0] + k * step[0]));
+        }
+        return n;
+    }
+};
 
 // Partial statistics of one channel: mean as hi + lo, and the sum of squared deviations from it.
 // Means that lie far from zero would otherwise round away what tells them apart.
@@ -102,40 +182,25 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_partial(const NormArgs a) 
             q.v[i] = __ffma2_rn(d, d, q.v[i]);
         }
     };
-    Pack<T, V> in[kBatch];
-    for (int k0 = 0; k0 < mine; k0 += kBatch) {
-        const int have = min(kBatch, mine - k0);
-        if (have == kBatch) {
+    constexpr size_t kMerge = sizeof(Stat) * (kThreads / 32) * 32 * V + 4 * kThreads;
+    __shared__ __align__(16) unsigned char smem[Stream<T, V, 1>::kSmem > kMerge ? Stream<T, V, 1>::kSmem : kMerge];
+    Stream<T, V, 1> rows;
+    rows.at[0] = x;
+    rows.step[0] = step;
+    rows.start(smem, mine);
+    const int m = rows.peek([&](const Pack<T, V>& in) {
+        Acc<V> f;
+        unpack_acc<T, V>(in, f);
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) in[k] = load_pack<T, V>(x + k * step);
-        } else {
+        for (int i = 0; i < H; ++i) sh.v[i] = __fadd2_rn(sh.v[i], f.v[i]);
+    });
+    if (m > 0) {
+        const float f = -1.0f / m;
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (k < have) in[k] = load_pack<T, V>(x + k * step);
-        }
-        x += kBatch * step;
-        if (k0 == 0) {
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (k < have) {
-                    Acc<V> f;
-                    unpack_acc<T, V>(in[k], f);
-#pragma unroll
-                    for (int i = 0; i < H; ++i) sh.v[i] = __fadd2_rn(sh.v[i], f.v[i]);
-                }
-            const float f = -1.0f / have;
-#pragma unroll
-            for (int i = 0; i < H; ++i) sh.v[i] = __fmul2_rn(sh.v[i], make_float2(f, f));
-        }
-        if (have == kBatch) {
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) add(in[k]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (k < have) add(in[k]);
-        }
+        for (int i = 0; i < H; ++i) sh.v[i] = __fmul2_rn(sh.v[i], make_float2(f, f));
     }
+    rows.run([&](const Pack<T, V>(&in)[1]) { add(in[0]); });
+    __syncthreads();  // the rows' slots are used again below
     float cnt = (float)mine;
     Stat st[V];
     {
@@ -160,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_partial(const NormArgs a) 
         }
         cnt += nb;
     }
-    __shared__ Stat sm[kThreads / 32][32 * V];
-    __shared__ float sn[kThreads / 32][32];
+    Stat(*sm)[32 * V] = reinterpret_cast<Stat(*)[32 * V]>(smem);
+    float(*sn)[32] = reinterpret_cast<float(*)[32]>(smem + sizeof(Stat) * (kThreads / 32) * 32 * V);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     sn[warp][lane] = cnt;
 #pragma unroll
@@ -270,18 +335,16 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const NormArgs a) {
         if constexpr (V == 1) *to = from_f<T>(f.v[0].x);
         else store_pairs<T, V>(to, f.v);
     };
-    constexpr int U = kBatch;
-    int k = 0;
-    for (; k + U <= mine; k += U) {
-        Pack<T, V> in[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j) in[j] = load_pack<T, V>(x + j * xs);
-        x += U * xs;
-#pragma unroll
-        for (int j = 0; j < U; ++j) put(in[j], y + j * ys);
-        y += U * ys;
-    }
-    for (; k < mine; ++k, x += xs, y += ys) put(load_pack<T, V>(x), y);
+    __shared__ __align__(16) unsigned char smem[Stream<T, V, 1>::kSmem];
+    Stream<T, V, 1> rows;
+    rows.at[0] = x;
+    rows.step[0] = xs;
+    rows.start(smem, mine);
+    rows.run([&](const Pack<T, V>(&in)[1]) {
+        put(in[0], y);
+        y += ys;
+    });
+    int k = mine;
     const Pack<T, V> zero{};
     for (; p.ty + k * p.TY < r1 - r0; ++k, y += ys) *reinterpret_cast<Pack<T, V>*>(y) = zero;
 }
@@ -328,6 +391,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_bwd_partial(const NormArgs
     const Place p = place<V>(a, blockIdx.x);
     const int n = valid_rows(a, p.b);
     const int r0 = min(p.ch * a.rows, n), r1 = min(r0 + a.rows, n);
+    constexpr size_t kMerge = sizeof(float) * (kThreads / 32) * 32 * V * NS;
+    __shared__ __align__(16) unsigned char smem[Stream<T, V, 2>::kSmem > kMerge ? Stream<T, V, 2>::kSmem : kMerge];
     float2 acc[NS][H];
 #pragma unroll
     for (int j = 0; j < NS; ++j)
@@ -357,21 +422,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_bwd_partial(const NormArgs
                 }
             }
         };
-        int k = 0;
-        for (; k + kBatch <= mine; k += kBatch) {
-            Pack<T, V> in[kBatch], gr[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                in[j] = load_pack<T, V>(x + j * xs);
-                gr[j] = load_pack<T, V>(dy + j * gs);
-            }
-            x += kBatch * xs;
-            dy += kBatch * gs;
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) add(in[j], gr[j]);
-        }
-        for (; k < mine; ++k, x += xs, dy += gs) add(load_pack<T, V>(x), load_pack<T, V>(dy));
+        Stream<T, V, 2> rows;
+        rows.at[0] = x;
+        rows.at[1] = dy;
+        rows.step[0] = xs;
+        rows.step[1] = gs;
+        rows.start(smem, mine);
+        rows.run([&](const Pack<T, V>(&in)[2]) { add(in[0], in[1]); });
     }
+    __syncthreads();  // the rows' slots are used again below
     for (int off = 16; off >= a.tx; off >>= 1) {
 #pragma unroll
         for (int j = 0; j < NS; ++j)
@@ -381,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_bwd_partial(const NormArgs
                 acc[j][i].y += __shfl_xor_sync(0xffffffffu, acc[j][i].y, off);
             }
     }
-    __shared__ float sm[kThreads / 32][32 * V * NS];
+    float(*sm)[32 * V * NS] = reinterpret_cast<float(*)[32 * V * NS]>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto part = [&](int i, int j) { return V == 1 || i % 2 == 0 ? acc[j][i / 2].x : acc[j][i / 2].y; };
 #pragma unroll
@@ -506,21 +565,18 @@ __global__ void __launch_bounds__(kThreads, 3) k_norm_bwd_apply(const NormArgs a
         if constexpr (V == 1) *to = from_f<T>(f.v[0].x);
         else store_pairs<T, V>(to, f.v);
     };
-    int k = 0;
-    for (; k + kBatch <= mine; k += kBatch) {
-        Pack<T, V> in[kBatch], gr[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            in[j] = load_pack<T, V>(x + j * xs);
-            gr[j] = load_pack<T, V>(dy + j * gs);
-        }
-        x += kBatch * xs;
-        dy += kBatch * gs;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) put(in[j], gr[j], dx + j * os);
-        dx += kBatch * os;
-    }
-    for (; k < mine; ++k, x += xs, dy += gs, dx += os) put(load_pack<T, V>(x), load_pack<T, V>(dy), dx);
+    __shared__ __align__(16) unsigned char smem[Stream<T, V, 2>::kSmem];
+    Stream<T, V, 2> rows;
+    rows.at[0] = x;
+    rows.at[1] = dy;
+    rows.step[0] = xs;
+    rows.step[1] = gs;
+    rows.start(smem, mine);
+    rows.run([&](const Pack<T, V>(&in)[2]) {
+        put(in[0], in[1], dx);
+        dx += os;
+    });
+    int k = mine;
     const Pack<T, V> zero{};
     for (; p.ty + k * p.TY < r1 - r0; ++k, dx += os) *reinterpret_cast<Pack<T, V>*>(dx) = zero;
 }
