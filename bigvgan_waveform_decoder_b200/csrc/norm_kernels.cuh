@@ -142,39 +142,58 @@ struct FastDiv {
 };
 __device__ __forceinline__ unsigned operator/(unsigned n, FastDiv f) { return f.d == 1 ? n : __umulhi(n, f.mul); }
 
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+
+// v within [-c, c]; NaN stays NaN.
+__device__ __forceinline__ float clamp_nan(float v, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(-c));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(r) : "f"(c));
+    return r;
+}
+
 // sin(theta) and cos(theta) up to a common sign, theta = alpha u: what sin^2 and sin cos need, both
-// of period pi.  fp32 tensors: the phase is reduced to [-pi/2, pi/2] by the Cody-Waite method (pi as
-// fp32(pi) plus the fp32 remainder, the product's rounding error carried along from one fma), then
-// the Taylor series (truncated terms below 7e-10).  16-bit tensors: the hardware sine, whose 2^-21
-// absolute error is far below their rounding; its argument loses |theta| 2^-24 as the product itself
-// does, so a reduction first would gain nothing.
-template <bool PRECISE>
-__device__ __forceinline__ void sin_cos_mod_pi(float alpha, float u, float* sn, float* cs) {
-    const float v = alpha * u;
-    if (PRECISE) {
-        const float e = fmaf(alpha, u, -v);
-        const float k = rintf(v * 0.318309886183790671538f);
-        float r = fmaf(-k, 3.14159274101257324219f, v);
-        r = fmaf(-k, -8.74227800037248297e-08f, r) + e;
-        const float r2 = r * r;
-        float p = 1.0f / 6227020800.0f;
-        p = fmaf(p, r2, -1.0f / 39916800.0f);
-        p = fmaf(p, r2, 1.0f / 362880.0f);
-        p = fmaf(p, r2, -1.0f / 5040.0f);
-        p = fmaf(p, r2, 1.0f / 120.0f);
-        p = fmaf(p, r2, -1.0f / 6.0f);
-        *sn = fmaf(r * r2, p, r);
-        float q = -1.0f / 87178291200.0f;
-        q = fmaf(q, r2, 1.0f / 479001600.0f);
-        q = fmaf(q, r2, -1.0f / 3628800.0f);
-        q = fmaf(q, r2, 1.0f / 40320.0f);
-        q = fmaf(q, r2, -1.0f / 720.0f);
-        q = fmaf(q, r2, 1.0f / 24.0f);
-        q = fmaf(q, r2, -0.5f);
-        *cs = fmaf(q, r2, 1.0f);
-    } else {
-        *sn = __sinf(v);
-        *cs = __cosf(v);
+// of period pi; two values at a time in packed fp32x2 operations.
+//
+// fp32 tensors (PRECISE): the phase is reduced to [-pi/2, pi/2] by the Cody-Waite method (pi as
+// fp32(pi) plus the fp32 remainder, the product's rounding error carried along from one fma), then the
+// Taylor series (truncated terms below 7e-10).  k = rint(theta / pi) comes from adding and taking away
+// 1.5 2^23, right for |theta| below 2^22 pi; farther out fp32 leaves theta no fraction of a period, and
+// the clamp keeps the result a sine.
+//
+// 16-bit tensors: the hardware sine, whose 2^-21 absolute error is far below their rounding; its
+// argument loses |theta| 2^-24 as the product itself does, so a reduction first would gain nothing.
+template <bool PRECISE, bool COS>
+__device__ __forceinline__ void sin_cos_mod_pi(float2 alpha, float2 u, float2* sn, float2* cs) {
+    const float2 v = __fmul2_rn(alpha, u);
+    if (!PRECISE) {
+        *sn = make_float2(__sinf(v.x), __sinf(v.y));
+        if (COS) *cs = make_float2(__cosf(v.x), __cosf(v.y));
+        return;
+    }
+    const float2 e = __ffma2_rn(alpha, u, neg2(v));
+    const float2 k = __fadd2_rn(__ffma2_rn(v, both(0.318309886183790671538f), both(12582912.f)), both(-12582912.f));
+    float2 r = __ffma2_rn(k, both(-3.14159274101257324219f), v);
+    r = __fadd2_rn(__ffma2_rn(k, both(8.74227800037248297e-08f), r), e);
+    r = make_float2(clamp_nan(r.x, 1.6f), clamp_nan(r.y, 1.6f));
+    const float2 r2 = __fmul2_rn(r, r);
+    float2 p = both(1.0f / 6227020800.0f);
+    p = __ffma2_rn(p, r2, both(-1.0f / 39916800.0f));
+    p = __ffma2_rn(p, r2, both(1.0f / 362880.0f));
+    p = __ffma2_rn(p, r2, both(-1.0f / 5040.0f));
+    p = __ffma2_rn(p, r2, both(1.0f / 120.0f));
+    p = __ffma2_rn(p, r2, both(-1.0f / 6.0f));
+    *sn = __ffma2_rn(__fmul2_rn(r, r2), p, r);
+    if (COS) {
+        float2 q = both(-1.0f / 87178291200.0f);
+        q = __ffma2_rn(q, r2, both(1.0f / 479001600.0f));
+        q = __ffma2_rn(q, r2, both(-1.0f / 3628800.0f));
+        q = __ffma2_rn(q, r2, both(1.0f / 40320.0f));
+        q = __ffma2_rn(q, r2, both(-1.0f / 720.0f));
+        q = __ffma2_rn(q, r2, both(1.0f / 24.0f));
+        q = __ffma2_rn(q, r2, both(-0.5f));
+        *cs = __ffma2_rn(q, r2, both(1.0f));
     }
 }
 
@@ -192,79 +211,42 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 // 1 / (1 + e^-u).  16-bit tensors take the hardware's exponential and reciprocal (each a few ulp;
 // results below 2^-126 become 0), without the scaling that keeps subnormal numbers.
 template <bool PRECISE>
-__device__ __forceinline__ float sigmoid(float u) {
-    if (PRECISE) return 1.0f / (1.0f + expf(-u));
-    return rcp_ftz(1.0f + ex2_ftz(-1.44269504088896341f * u));
+__device__ __forceinline__ float2 sigmoid(float2 u) {
+    if (PRECISE) return make_float2(1.0f / (1.0f + expf(-u.x)), 1.0f / (1.0f + expf(-u.y)));
+    const float2 t = __fmul2_rn(u, both(-1.44269504088896341f));
+    const float2 e = __fadd2_rn(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), both(1.f));
+    return make_float2(rcp_ftz(e.x), rcp_ftz(e.y));
 }
 
-// y = act(u); ib = 1 / (beta + 1e-9)
+// y = act(u) of two neighbouring channels; ib = 1 / (beta + 1e-9)
 template <int ACT, bool PRECISE>
-__device__ __forceinline__ float act_fwd(float u, float al, float ib) {
-    if (ACT == MH3A_ACT_SILU) return u * sigmoid<PRECISE>(u);
+__device__ __forceinline__ float2 act_fwd(float2 u, float2 al, float2 ib) {
+    if (ACT == MH3A_ACT_SILU) return __fmul2_rn(u, sigmoid<PRECISE>(u));
     if (ACT == MH3A_ACT_SNAKE_BETA) {
-        float sn, cs;
-        sin_cos_mod_pi<PRECISE>(al, u, &sn, &cs);
-        return fmaf(sn * sn, ib, u);
+        float2 sn, cs;
+        sin_cos_mod_pi<PRECISE, false>(al, u, &sn, &cs);
+        return __ffma2_rn(__fmul2_rn(sn, sn), ib, u);
     }
     return u;
-}
-
-// The same for a pair, by packed fp32x2 operations.
-template <int ACT, bool PRECISE>
-__device__ __forceinline__ float2 act_fwd2(float2 u, float2 al, float2 ib) {
-    if (PRECISE || ACT == MH3A_ACT_NONE)
-        return make_float2(act_fwd<ACT, PRECISE>(u.x, al.x, ib.x), act_fwd<ACT, PRECISE>(u.y, al.y, ib.y));
-    if (ACT == MH3A_ACT_SILU) {
-        const float2 t = __fmul2_rn(u, make_float2(-1.44269504088896341f, -1.44269504088896341f));
-        const float2 e = __fadd2_rn(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), make_float2(1.f, 1.f));
-        return __fmul2_rn(u, make_float2(rcp_ftz(e.x), rcp_ftz(e.y)));
-    }
-    const float2 v = __fmul2_rn(al, u);
-    const float2 sn = make_float2(__sinf(v.x), __sinf(v.y));
-    return __ffma2_rn(__fmul2_rn(sn, sn), ib, u);
 }
 
 // act'(u), and for SnakeBeta the factors of dalpha and dbeta: dalpha = sum dy *pa,
 // dbeta = -sum dy *pb (1/beta^2 follows once, after the sum).
 template <int ACT, bool PRECISE>
-__device__ __forceinline__ float act_slope(float u, float al, float ib, float* pa, float* pb) {
+__device__ __forceinline__ float2 act_slope(float2 u, float2 al, float2 ib, float2* pa, float2* pb) {
     if (ACT == MH3A_ACT_SILU) {
-        const float s = sigmoid<PRECISE>(u);
-        return s * fmaf(u, 1.0f - s, 1.0f);
+        const float2 s = sigmoid<PRECISE>(u);
+        return __fmul2_rn(s, __ffma2_rn(u, __ffma2_rn(s, both(-1.f), both(1.f)), both(1.f)));
     }
     if (ACT == MH3A_ACT_SNAKE_BETA) {
-        float sn, cs;
-        sin_cos_mod_pi<PRECISE>(al, u, &sn, &cs);
-        const float s2 = 2.0f * sn * cs * ib;  // sin(2 alpha u) / beta
-        *pa = u * s2;
-        *pb = sn * sn;
-        return fmaf(al, s2, 1.0f);
+        float2 sn, cs;
+        sin_cos_mod_pi<PRECISE, true>(al, u, &sn, &cs);
+        const float2 s2 = __fmul2_rn(__fmul2_rn(__fadd2_rn(sn, sn), cs), ib);  // sin(2 alpha u) / beta
+        *pa = __fmul2_rn(u, s2);
+        *pb = __fmul2_rn(sn, sn);
+        return __ffma2_rn(al, s2, both(1.f));
     }
-    return 1.0f;
-}
-
-// The same for a pair.
-template <int ACT, bool PRECISE>
-__device__ __forceinline__ float2 act_slope2(float2 u, float2 al, float2 ib, float2* pa, float2* pb) {
-    if (PRECISE || ACT == MH3A_ACT_NONE) {
-        float2 s;
-        s.x = act_slope<ACT, PRECISE>(u.x, al.x, ib.x, &pa->x, &pb->x);
-        s.y = act_slope<ACT, PRECISE>(u.y, al.y, ib.y, &pa->y, &pb->y);
-        return s;
-    }
-    const float2 one = make_float2(1.f, 1.f);
-    if (ACT == MH3A_ACT_SILU) {
-        const float2 t = __fmul2_rn(u, make_float2(-1.44269504088896341f, -1.44269504088896341f));
-        const float2 e = __fadd2_rn(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), one);
-        const float2 s = make_float2(rcp_ftz(e.x), rcp_ftz(e.y));
-        return __fmul2_rn(s, __ffma2_rn(u, __ffma2_rn(s, make_float2(-1.f, -1.f), one), one));
-    }
-    const float2 v = __fmul2_rn(al, u);
-    const float2 sn = make_float2(__sinf(v.x), __sinf(v.y)), cs = make_float2(__cosf(v.x), __cosf(v.y));
-    const float2 s2 = __fmul2_rn(__fmul2_rn(__fadd2_rn(sn, sn), cs), ib);
-    *pa = __fmul2_rn(u, s2);
-    *pb = __fmul2_rn(sn, sn);
-    return __ffma2_rn(al, s2, one);
+    return both(1.f);
 }
 
 // Sums of one channel in the backward pass: 0 du, 1 du xh, 2 dy * (factor of dalpha), 3 dy * (factor

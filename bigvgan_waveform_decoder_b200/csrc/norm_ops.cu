@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const NormArgs a) {
         for (int i = 0; i < H; ++i) {
             const float2 u = __ffma2_rn(__fadd2_rn(f.v[i], make_float2(mu[2 * i], mu[2 * i + 1])), make_float2(sc[2 * i], sc[2 * i + 1]),
                                         make_float2(bi[2 * i], bi[2 * i + 1]));
-            f.v[i] = act_fwd2<ACT, kPrecise>(u, make_float2(al[2 * i], al[2 * i + 1]), make_float2(ib[2 * i], ib[2 * i + 1]));
+            f.v[i] = act_fwd<ACT, kPrecise>(u, make_float2(al[2 * i], al[2 * i + 1]), make_float2(ib[2 * i], ib[2 * i + 1]));
         }
         if constexpr (V == 1) *to = from_f<T>(f.v[0].x);
         else store_pairs<T, V>(to, f.v);
@@ -378,7 +378,7 @@ struct BwdParams {
     __device__ __forceinline__ float2 slope(float2 xh, int i, float2* pa, float2* pb) const {
         constexpr bool kSnake = ACT == MH3A_ACT_SNAKE_BETA;
         const float2 u = __ffma2_rn(xh, w[i], bi[i]);
-        return act_slope2<ACT, PRECISE>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u, pa, pb);
+        return act_slope<ACT, PRECISE>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u, pa, pb);
     }
 };
 

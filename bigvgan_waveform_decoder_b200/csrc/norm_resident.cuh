@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 const float2 u = __ffma2_rn(__fadd2_rn(f[i], mu[i]), sc[i], bi[i]);
-                f[i] = act_fwd2<ACT, kPrecise>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u);
+                f[i] = act_fwd<ACT, kPrecise>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u);
             }
             store_pairs<T, V>(y, f);
         }
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kResThreads) k_norm_bwd_resident(const NormArg
                 const float2 xh = __fmul2_rn(__fadd2_rn(f[i], mu[WHOLE ? 0 : i]), rs[WHOLE ? 0 : i]);
                 const float2 u = __ffma2_rn(xh, w[i], bi[i]);
                 float2 pa, pb;
-                const float2 du = __fmul2_rn(d[i], act_slope2<ACT, kPrecise>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u, &pa, &pb));
+                const float2 du = __fmul2_rn(d[i], act_slope<ACT, kPrecise>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u, &pa, &pb));
                 acc[0][i] = __fadd2_rn(acc[0][i], du);
                 acc[1][i] = __ffma2_rn(du, xh, acc[1][i]);
                 if constexpr (NS == 4) {
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kResThreads) k_norm_bwd_resident(const NormArg
                 if (!kPrecise) {
                     const float2 u = __ffma2_rn(xh, w[i], bi[i]);
                     float2 pa, pb;
-                    du = __fmul2_rn(du, act_slope2<ACT, kPrecise>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u, &pa, &pb));
+                    du = __fmul2_rn(du, act_slope<ACT, kPrecise>(u, kSnake ? al[i] : u, kSnake ? ib[i] : u, &pa, &pb));
                 }
                 f[i] = __fmul2_rn(rs[j], __ffma2_rn(xh, m2[j], __ffma2_rn(du, w[i], m1[j])));
             }

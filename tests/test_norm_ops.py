@@ -166,6 +166,27 @@ def test_not_finite_values_stay_in_their_group(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", (5, 1500, 60000))
+def test_phases_beyond_the_period(T, dtype):
+    """SnakeBeta of huge u: fp32 (and its product with alpha) leaves no fraction of a period, so the sine is
+    arbitrary but stays one; y - u is within [0, 1 / beta], the slope within 1 +- alpha / beta."""
+    Cn, G = 16, 2
+    x, w, b, al, be = case(1, T, Cn, "snake_beta", "fp32", seed=13)
+    x, w = x.to(TYPES[dtype]), w.sign() * 10.0 ** torch.linspace(1, 4 if dtype == "fp16" else 14, Cn, device="cuda")
+    y, m, r = pkg.group_norm_act(x, G, w, b, act="snake_beta", alpha=al, beta=be)
+    u = R.norm_forward(x, G, w, b, "none", None, None, 1e-5, None)[0]
+    slack = torch.finfo(y.dtype).eps / 2 * (u.abs() + 2) + 64 * R.F24 * (u.abs() + 10 * w.double().abs())
+    d = y.double() - u
+    assert torch.all(d >= -slack) and torch.all(d <= 1.001 / be.double() + slack)
+    dx, dw, db, da, dbe = pkg.group_norm_act_backward(torch.ones_like(x), x, m, r, G, w, b, act="snake_beta", alpha=al, beta=be)
+    for t in (dx.float(), dw, db, da, dbe):
+        assert bool(torch.isfinite(t).all()) or dtype == "fp16"
+    assert torch.all(db.double().abs() <= 1.01 * T * (1 + al.double() / be.double()))
+    assert torch.all((dbe <= 0) & (dbe.double() >= -1.01 * T / be.double() ** 2))
+
+
+@pytest.mark.gpu
 def test_without_parameters_and_with_some():
     x, w, b, al, be = case(2, 60, 48, "snake_beta", "fp32", seed=6)
     dy = torch.randn_like(x)
