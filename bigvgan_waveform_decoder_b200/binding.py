@@ -147,7 +147,7 @@ def load():
     L.mh3a_last_error.restype = C.c_char_p
     ll, i, sz = C.c_longlong, C.c_int, C.c_size_t
     norm = C.POINTER(mh3a_norm)
-    L.mh3a_group_norm_act_workspace.argtypes = [norm, i]
+    L.mh3a_group_norm_act_workspace.argtypes = [norm, i, i]
     L.mh3a_group_norm_act_workspace.restype = sz
     L.mh3a_group_norm_act.argtypes = [norm, vp, ll, ll, vp, vp, vp, vp, sz, vp]
     L.mh3a_group_norm_act.restype = i

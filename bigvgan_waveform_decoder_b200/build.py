@@ -74,7 +74,7 @@ def build_ops(force: bool = False, verbose: bool = False) -> str:
     cmd = [NVCC, *FLAGS[:2], "-shared", "-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_ops",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *[f for i in inc for f in ("-isystem", i)],
            OPS_SRC, "-o", tmp, "-L", HERE, "-l:libmh3a.so", "-Xlinker", "-rpath=$ORIGIN", "-L", lib, "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", "--cudart", "none"]
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "--cudart", "none"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)

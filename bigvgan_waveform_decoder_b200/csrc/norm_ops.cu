@@ -673,6 +673,46 @@ bool go_resident(const NormArgs& a, const Resident& r, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, Kern, a, r) == cudaSuccess;
 }
 
+// Scratch of the general form with vectors of V channels.
+size_t general_bytes(NormArgs a, int act, int backward, int V) {
+    plan_general(&a, V, backward ? kBwdPerSm : kFwdPerSm);
+    const long long ns = act == MH3A_ACT_SNAKE_BETA ? 4 : 2;
+    long long floats = (long long)a.B * a.chunks * a.C * (backward ? ns : 4);
+    if (backward) floats += ((long long)a.B * a.C * ns + 3) / 4 * 4 + 2LL * a.B * a.G;
+    return ((size_t)floats * 4 + 255) / 256 * 256;
+}
+
+// The way a call goes, by its sizes and whether everything is aligned to whole vectors.
+struct Way {
+    bool resident;
+    Resident r;
+    size_t bytes;  // scratch
+};
+
+template <typename T>
+Way way(const NormArgs& a, int act, int backward, bool vec) {
+    constexpr int V = 16 / sizeof(T);
+    Way w{};
+    const int ns = act == MH3A_ACT_SNAKE_BETA ? 4 : 2;
+    auto extra = [&](int W, int S) { return backward ? res_bwd_extra(W, a.D, V, S, ns) : res_fwd_extra(W, a.D, V, S); };
+    w.resident = vec && plan_resident(a, V, sizeof(T), (backward ? 2 : 1) * sizeof(T), extra, &w.r);
+    if (w.resident) w.bytes = backward && a.B > 1 ? ((size_t)a.B * a.C * ns * 4 + 255) / 256 * 256 : 0;
+    else w.bytes = general_bytes(a, act, backward, !vec ? 1 : backward ? 4 : V);
+    return w;
+}
+
+Way way(const NormArgs& a, int dtype, int act, int backward, bool vec) {
+    switch (dtype) {
+        case MH3A_DTYPE_F32: return way<float>(a, act, backward, vec);
+        case MH3A_DTYPE_F16: return way<__half>(a, act, backward, vec);
+        default: return way<__nv_bfloat16>(a, act, backward, vec);
+    }
+}
+
+bool scratch_ok(const void* workspace, size_t have, size_t need) {
+    return need == 0 || (workspace && aligned(workspace, 16) && have >= need);
+}
+
 template <typename T, int V, int ACT>
 bool forward_resident(const NormArgs& a, const Resident& r, cudaStream_t s) {
     return a.D % V == 0 ? go_resident<k_norm_resident<T, V, ACT, true>>(a, r, s)
@@ -692,15 +732,13 @@ bool forward_general(const NormArgs& a, int act, cudaStream_t s) {
 }
 
 template <typename T>
-bool forward(NormArgs& a, int act, bool vec, cudaStream_t s) {
+bool forward(NormArgs& a, const Way& w, int act, bool vec, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    Resident r;
-    auto extra = [&](int W, int S) { return res_fwd_extra(W, a.D, V, S); };
-    if (vec && plan_resident(a, V, sizeof(T), sizeof(T), extra, &r)) {
+    if (w.resident) {
         switch (act) {
-            case MH3A_ACT_SILU: return forward_resident<T, V, MH3A_ACT_SILU>(a, r, s);
-            case MH3A_ACT_SNAKE_BETA: return forward_resident<T, V, MH3A_ACT_SNAKE_BETA>(a, r, s);
-            default: return forward_resident<T, V, MH3A_ACT_NONE>(a, r, s);
+            case MH3A_ACT_SILU: return forward_resident<T, V, MH3A_ACT_SILU>(a, w.r, s);
+            case MH3A_ACT_SNAKE_BETA: return forward_resident<T, V, MH3A_ACT_SNAKE_BETA>(a, w.r, s);
+            default: return forward_resident<T, V, MH3A_ACT_NONE>(a, w.r, s);
         }
     }
     plan_general(&a, vec ? V : 1, kFwdPerSm);
@@ -722,13 +760,11 @@ bool backward_general(const NormArgs& a, cudaStream_t s) {
 }
 
 template <typename T, int ACT>
-bool backward_act(NormArgs& a, bool vec, cudaStream_t s) {
+bool backward_act(NormArgs& a, const Way& w, bool vec, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T), NS = kSums<ACT>;
-    Resident r;
-    auto extra = [&](int W, int S) { return res_bwd_extra(W, a.D, V, S, NS); };
-    if (vec && plan_resident(a, V, sizeof(T), 2 * sizeof(T), extra, &r)) {
-        const bool ok = a.D % V == 0 ? go_resident<k_norm_bwd_resident<T, V, ACT, true>>(a, r, s)
-                                     : go_resident<k_norm_bwd_resident<T, V, ACT, false>>(a, r, s);
+    if (w.resident) {
+        const bool ok = a.D % V == 0 ? go_resident<k_norm_bwd_resident<T, V, ACT, true>>(a, w.r, s)
+                                     : go_resident<k_norm_bwd_resident<T, V, ACT, false>>(a, w.r, s);
         if (!ok || a.B == 1) return ok;
         return go(k_norm_bwd_final, (a.C + 255LL) / 256, 256, s, a, (const float*)a.ws, (float2*)nullptr, NS, 0);
     }
@@ -739,11 +775,11 @@ bool backward_act(NormArgs& a, bool vec, cudaStream_t s) {
 }
 
 template <typename T>
-bool backward(NormArgs& a, int act, bool vec, cudaStream_t s) {
+bool backward(NormArgs& a, const Way& w, int act, bool vec, cudaStream_t s) {
     switch (act) {
-        case MH3A_ACT_SILU: return backward_act<T, MH3A_ACT_SILU>(a, vec, s);
-        case MH3A_ACT_SNAKE_BETA: return backward_act<T, MH3A_ACT_SNAKE_BETA>(a, vec, s);
-        default: return backward_act<T, MH3A_ACT_NONE>(a, vec, s);
+        case MH3A_ACT_SILU: return backward_act<T, MH3A_ACT_SILU>(a, w, vec, s);
+        case MH3A_ACT_SNAKE_BETA: return backward_act<T, MH3A_ACT_SNAKE_BETA>(a, w, vec, s);
+        default: return backward_act<T, MH3A_ACT_NONE>(a, w, vec, s);
     }
 }
 
@@ -777,21 +813,6 @@ NormArgs base_args(const mh3a_norm* p) {
     return a;
 }
 
-// Scratch of the general form, the largest over its vector widths; the resident form needs less (the
-// per-channel sums of each item).
-size_t general_bytes(const mh3a_norm* p, int backward) {
-    size_t most = 0;
-    for (int V : {1, 4, 16 / elem_bytes(p->dtype)}) {
-        NormArgs a = base_args(p);
-        plan_general(&a, V, backward ? kBwdPerSm : kFwdPerSm);
-        const long long ns = p->act == MH3A_ACT_SNAKE_BETA ? 4 : 2;
-        long long floats = (long long)a.B * a.chunks * a.C * (backward ? ns : 4);
-        if (backward) floats += ((long long)a.B * a.C * ns + 3) / 4 * 4 + 2LL * a.B * a.G;
-        most = std::max(most, (size_t)floats * 4);
-    }
-    return (most + 255) / 256 * 256;
-}
-
 // Whether whole vectors can be used: parameters are then read by 16-byte loads.
 bool params_fit(const NormArgs& a) {
     return aligned(a.weight, 16) && aligned(a.bias, 16) && aligned(a.alpha, 16) && aligned(a.beta, 16);
@@ -805,8 +826,13 @@ bool strides_fit(long long b, long long r, int V) { return b % V == 0 && r % V =
 using namespace mh3a;
 using namespace mh3a::norm;
 
-extern "C" MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward) {
-    return check(p) == MH3A_OK ? general_bytes(p, backward) : 0;
+extern "C" MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward, int aligned_all) {
+    if (check(p) != MH3A_OK) return 0;
+    const NormArgs a = base_args(p);
+    const size_t any = way(a, p->dtype, p->act, backward, false).bytes;
+    const bool vec = p->C % (16 / elem_bytes(p->dtype)) == 0;
+    const size_t whole = vec ? way(a, p->dtype, p->act, backward, true).bytes : any;
+    return aligned_all ? whole : std::max(any, whole);
 }
 
 extern "C" MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const void* x, long long x_batch_stride,
@@ -817,7 +843,6 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const vo
     if (!x || !y || !mean || !rstd || x_batch_stride < 0 || x_row_stride < 0) return MH3A_ERR_INVALID_ARG;
     const int e = elem_bytes(p->dtype), V = 16 / e;
     if (!aligned(x, e) || !aligned(y, e) || !aligned(mean, 4) || !aligned(rstd, 4)) return MH3A_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < general_bytes(p, 0)) return MH3A_ERR_INVALID_ARG;
     NormArgs a = base_args(p);
     a.x = x;
     a.xb = x_batch_stride;
@@ -827,12 +852,14 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const vo
     a.rstd = rstd;
     a.ws = static_cast<float*>(workspace);
     const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(y, 16) && strides_fit(a.xb, a.xr, V) && params_fit(a);
+    const Way w = way(a, p->dtype, p->act, 0, vec);
+    if (!scratch_ok(workspace, workspace_bytes, w.bytes)) return MH3A_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     bool ok;
     switch (p->dtype) {
-        case MH3A_DTYPE_F32: ok = forward<float>(a, p->act, vec, s); break;
-        case MH3A_DTYPE_F16: ok = forward<__half>(a, p->act, vec, s); break;
-        default: ok = forward<__nv_bfloat16>(a, p->act, vec, s);
+        case MH3A_DTYPE_F32: ok = forward<float>(a, w, p->act, vec, s); break;
+        case MH3A_DTYPE_F16: ok = forward<__half>(a, w, p->act, vec, s); break;
+        default: ok = forward<__nv_bfloat16>(a, w, p->act, vec, s);
     }
     return ok ? MH3A_OK : launch_failed("mh3a_group_norm_act");
 }
@@ -850,7 +877,6 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p,
     if (p->act != MH3A_ACT_SNAKE_BETA && (dalpha || dbeta)) return MH3A_ERR_INVALID_ARG;
     const int e = elem_bytes(p->dtype), V = 16 / e;
     if (!aligned(x, e) || !aligned(dy, e) || !aligned(dx, e)) return MH3A_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < general_bytes(p, 1)) return MH3A_ERR_INVALID_ARG;
     NormArgs a = base_args(p);
     a.x = x;
     a.xb = x_batch_stride;
@@ -868,12 +894,14 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p,
     a.ws = static_cast<float*>(workspace);
     const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(dx, 16) &&
                      strides_fit(a.xb, a.xr, V) && strides_fit(a.gb, a.gr, V) && params_fit(a);
+    const Way w = way(a, p->dtype, p->act, 1, vec);
+    if (!scratch_ok(workspace, workspace_bytes, w.bytes)) return MH3A_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     bool ok;
     switch (p->dtype) {
-        case MH3A_DTYPE_F32: ok = backward<float>(a, p->act, vec, s); break;
-        case MH3A_DTYPE_F16: ok = backward<__half>(a, p->act, vec, s); break;
-        default: ok = backward<__nv_bfloat16>(a, p->act, vec, s);
+        case MH3A_DTYPE_F32: ok = backward<float>(a, w, p->act, vec, s); break;
+        case MH3A_DTYPE_F16: ok = backward<__half>(a, w, p->act, vec, s); break;
+        default: ok = backward<__nv_bfloat16>(a, w, p->act, vec, s);
     }
     return ok ? MH3A_OK : launch_failed("mh3a_group_norm_act_backward");
 }

@@ -2,6 +2,7 @@
 // allocation around the C ABI of include/mh3a.h, nothing else.  It is compiled code because the
 // smallest calls take 3 to 4 us on the GPU: the same marshalling in Python took 19 us a call.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/extension.h>
@@ -77,7 +78,7 @@ int dtype_of(at::ScalarType t) {
 }
 
 Tensor empty(at::IntArrayRef size, at::ScalarType type, const c10::Device& device) {
-    return at::empty(size, at::TensorOptions().dtype(type).device(device));
+    return Tensor(at::detail::empty_cuda(size, type, device, std::nullopt));
 }
 
 // A contiguous tensor of a type and shape on the call's device.
@@ -87,6 +88,16 @@ void check_plain(const char* what, const char* name, const Tensor& t, const c10:
         refuse(what, MH3A_ERR_INVALID_ARG, name, " is not a contiguous ", type, " tensor on ", device);
     if (t.sizes() != shape) refuse(what, MH3A_ERR_SHAPE, name, " is ", t.sizes(), ": ", shape, " is wanted");
 }
+
+// Whether a tensor starts on a 16-byte boundary with strides of whole 16 bytes (but the last).
+bool aligned16(const Tensor& t) {
+    if (reinterpret_cast<uintptr_t>(t.data_ptr()) % 16) return false;
+    const int64_t per = 16 / t.element_size();
+    for (int64_t i = 0; i + 1 < t.dim(); ++i)
+        if (t.stride(i) % per) return false;
+    return true;
+}
+bool aligned16(const Opt& t) { return !t || aligned16(*t); }
 
 template <typename T>
 T* data(const Opt& t) { return t ? static_cast<T*>(t->data_ptr()) : nullptr; }
@@ -142,10 +153,12 @@ std::tuple<Tensor, Tensor, Tensor> group_norm_act(const Tensor& x, int64_t group
     const Launch on(device, stream);
     Tensor y = out ? *out : empty(x.sizes(), x.scalar_type(), device);
     Tensor mean = empty({p.B, groups}, at::kFloat, device), rstd = empty({p.B, groups}, at::kFloat, device);
-    const size_t n = mh3a_group_norm_act_workspace(&p, 0);
-    const Tensor ws = empty({(int64_t)n}, at::kByte, device);
+    const size_t n = mh3a_group_norm_act_workspace(
+        &p, 0, aligned16(x) && aligned16(y) && aligned16(weight) && aligned16(bias) && aligned16(alpha) && aligned16(beta));
+    Tensor ws;
+    if (n) ws = empty({(int64_t)n}, at::kByte, device);
     check(mh3a_group_norm_act(&p, x.data_ptr(), x.stride(0), x.stride(1), y.data_ptr(), mean.data_ptr<float>(),
-                              rstd.data_ptr<float>(), ws.data_ptr(), n, on.stream()),
+                              rstd.data_ptr<float>(), n ? ws.data_ptr() : nullptr, n, on.stream()),
           what);
     on.inputs({&x, opt(weight), opt(bias), opt(alpha), opt(beta), opt(lengths), opt(out)});
     on.outputs({&y, &mean, &rstd});
@@ -172,11 +185,13 @@ std::tuple<Tensor, Opt, Opt, Opt, Opt> group_norm_act_backward(const Tensor& dy,
     Opt grads[4];
     for (int i = 0; i < 4; ++i)
         if (*params[i]) grads[i] = empty({p.C}, at::kFloat, device);
-    const size_t n = mh3a_group_norm_act_workspace(&p, 1);
-    const Tensor ws = empty({(int64_t)n}, at::kByte, device);
+    const size_t n = mh3a_group_norm_act_workspace(
+        &p, 1, aligned16(x) && aligned16(dy) && aligned16(dx) && aligned16(weight) && aligned16(bias) && aligned16(alpha) && aligned16(beta));
+    Tensor ws;
+    if (n) ws = empty({(int64_t)n}, at::kByte, device);
     check(mh3a_group_norm_act_backward(&p, x.data_ptr(), x.stride(0), x.stride(1), dy.data_ptr(), dy.stride(0), dy.stride(1),
                                        mean.data_ptr<float>(), rstd.data_ptr<float>(), dx.data_ptr(), data<float>(grads[0]),
-                                       data<float>(grads[1]), data<float>(grads[2]), data<float>(grads[3]), ws.data_ptr(), n,
+                                       data<float>(grads[1]), data<float>(grads[2]), data<float>(grads[3]), n ? ws.data_ptr() : nullptr, n,
                                        on.stream()),
           what);
     on.inputs({&dy, &x, &mean, &rstd, opt(weight), opt(bias), opt(alpha), opt(beta), opt(lengths)});

@@ -338,8 +338,11 @@ typedef struct {
 } mh3a_norm;
 
 /* Scratch bytes of mh3a_group_norm_act (backward = 0) or mh3a_group_norm_act_backward
- * (backward = 1) for *p; 0 when *p is invalid.  The size depends on *p alone. */
-MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward);
+ * (backward = 1) for *p; 0 when the call needs none, or when *p is invalid.  aligned = 1 promises
+ * that x, y (dx, dy) and the parameters start on 16-byte boundaries and that the strides of x (and
+ * dy) are multiples of 16 bytes: the form that then serves smaller tensors needs no scratch forward
+ * and little backward.  With aligned = 0 the size serves any pointers and strides. */
+MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward, int aligned);
 
 /* Per item b and group g, over the item's valid rows and the group's channels:
  *   mean, rstd = 1 / sqrt(var + eps)  (biased variance),
@@ -348,7 +351,8 @@ MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward);
  * elements (strides >= 0; 0 repeats an item or a row).  y: device [B, T, C], contiguous, must not
  * overlap x.  mean, rstd: device [B, groups], what the backward pass needs.  An item of no valid
  * rows has mean 0 and var 0.  All arithmetic is fp32 (combining partial statistics: fp64), rounded once to the type of y.
- * `workspace`: device, 16-byte aligned, at least mh3a_group_norm_act_workspace(p, 0) bytes.
+ * `workspace`: device, 16-byte aligned, at least mh3a_group_norm_act_workspace(p, 0, aligned) bytes
+ * (NULL where that is 0).
  * Errors: MH3A_ERR_INVALID_ARG (NULL p, x, y, mean or rstd; unknown dtype or act; alpha or beta
  * missing for SnakeBeta; a negative stride; a pointer not aligned to its element type;
  * a workspace missing, too small or misaligned), MH3A_ERR_SHAPE (B, T, C or groups below 1, groups

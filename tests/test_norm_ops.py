@@ -318,26 +318,31 @@ def test_abi_refusals():
     """Every refusal comes before any device work (the pointers here are no device memory)."""
     L = Bd.load()
     p0, ok = C.byref(norm()), 1 << 20
-    size = L.mh3a_group_norm_act_workspace(p0, 0)
-    assert size > 0 and L.mh3a_group_norm_act_workspace(p0, 1) >= size
+    size = L.mh3a_group_norm_act_workspace(p0, 0, 0)
+    assert size > 0 and L.mh3a_group_norm_act_workspace(p0, 1, 0) > 0
+    assert L.mh3a_group_norm_act_workspace(p0, 0, 1) == 0 and 0 < L.mh3a_group_norm_act_workspace(p0, 1, 1)
+    large = C.byref(norm(B=16, T=20000, C=256, groups=32))
+    for backward in (0, 1):
+        some = L.mh3a_group_norm_act_workspace(large, backward, 1)
+        assert 0 < some <= L.mh3a_group_norm_act_workspace(large, backward, 0)
 
-    def fwd(p=None, x=ok, xb=240, xr=24, y=ok, mean=ok, rstd=ok, ws=ok, n=size):
+    def fwd(p=None, x=ok + 2, xb=240, xr=24, y=ok, mean=ok, rstd=ok, ws=ok, n=size):
         return L.mh3a_group_norm_act(None if p is None else C.byref(p), x, xb, xr, y, mean, rstd, ws, n, None)
 
     good = norm()
     assert fwd(None) == 1
     for kw in (dict(x=None), dict(y=None), dict(mean=None), dict(rstd=None), dict(ws=None), dict(n=size - 1), dict(xb=-1),
-               dict(xr=-1), dict(x=ok + 1), dict(y=ok + 1), dict(ws=ok + 8)):
+               dict(xr=-1), dict(x=ok + 1), dict(y=ok + 1), dict(ws=ok + 8), dict(x=ok, xr=25, ws=None)):
         assert fwd(good, **kw) == 1, kw
     for kw in (dict(dtype=3), dict(dtype=-1), dict(act=3), dict(act=-1), dict(act=2), dict(act=2, alpha=ok)):
         assert fwd(norm(**kw)) == 1, kw
-        assert L.mh3a_group_norm_act_workspace(C.byref(norm(**kw)), 0) == 0
+        assert L.mh3a_group_norm_act_workspace(C.byref(norm(**kw)), 0, 0) == 0
     for kw in (dict(B=0), dict(T=0), dict(C=0), dict(groups=0), dict(groups=5), dict(T=(1 << 30) + 1),
                dict(B=1 << 20, C=1 << 12, groups=1)):
         assert fwd(norm(**kw)) == 3, kw
-    n1 = L.mh3a_group_norm_act_workspace(p0, 1)
+    n1 = L.mh3a_group_norm_act_workspace(p0, 1, 0)
 
-    def bwd(p=None, x=ok, dy=ok, mean=ok, rstd=ok, dx=ok, da=None, ws=ok, n=n1, gb=240):
+    def bwd(p=None, x=ok + 2, dy=ok, mean=ok, rstd=ok, dx=ok, da=None, ws=ok, n=n1, gb=240):
         return L.mh3a_group_norm_act_backward(None if p is None else C.byref(p), x, 240, 24, dy, gb, 24, mean, rstd, dx, ok, ok,
                                               da, None, ws, n, None)
 
@@ -346,7 +351,7 @@ def test_abi_refusals():
                dict(n=n1 - 1), dict(gb=-1), dict(dy=ok + 1)):
         assert bwd(good, **kw) == 1, kw
     assert bwd(norm(groups=7)) == 3
-    assert L.mh3a_group_norm_act_workspace(None, 0) == 0
+    assert L.mh3a_group_norm_act_workspace(None, 0, 0) == 0
 
 
 def test_tensors_that_are_not_on_a_gpu_are_refused():
