@@ -271,6 +271,9 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                     tma_load_2d(to + kM * kBlock, &map_b, kb * kBlock, n0, full + s);
                 }
             }
+            // never expected: after a wait that ran out of time, the copies on their way are seen in
+            if (!ok)
+                for (int j = max(0, it - C::kStages); j < it; ++j) ptx::mbar_wait(full + j % C::kStages, (j / C::kStages) & 1);
         } else if (warp == 1) {
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);  // e4m3, fp32 sums
             int it = 0;

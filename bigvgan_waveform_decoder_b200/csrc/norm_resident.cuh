@@ -83,6 +83,24 @@ __device__ __forceinline__ void send16(uint32_t to, uint32_t bar, float4 v) {
                  "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
                  : "memory");
 }
+// Waits (up to a second) for the bytes that the peers send to this block's mbarrier.
+__device__ __forceinline__ bool wait_for_peers(uint64_t* bar) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i) {
+            uint32_t ok;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(ptx::smem_u32(bar))
+                : "memory");
+            if (ok) return true;
+        }
+        if (ptx::globaltimer_ns() - t0 > 1000000000ull) return false;
+    }
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
@@ -236,7 +254,7 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
             send16(peer_smem(ptx::smem_u32(inbox + p.rank * ng + g), lane), peer_smem(ptx::smem_u32(bar), lane),
                    make_float4(o.hi, o.lo, o.m2, o.n));
     }
-    const bool arrived = ptx::mbar_wait(bar, 0);  // so no peer sends to this block after it has ended
+    const bool arrived = wait_for_peers(bar);  // so no peer sends to this block after it has ended
     for (int g = warp; g < ng; g += kResThreads / 32) {
         Part o{0.f, 0.f, 0.f, 0.f};
         if (lane < r.S) o = inbox[lane * ng + g];
@@ -437,7 +455,7 @@ __global__ void __launch_bounds__(kResThreads) k_norm_bwd_resident(const NormArg
         for (int peer = 0; peer < r.S; ++peer)
             send16(peer_smem(ptx::smem_u32(inbox + p.rank * cols + c), peer), peer_smem(ptx::smem_u32(bar), peer), s);
     }
-    const bool arrived = ptx::mbar_wait(bar, 0);
+    const bool arrived = wait_for_peers(bar);
     for (int c = threadIdx.x; c < cols; c += kResThreads) {
         float s = 0.f;
         for (int k = 0; k < r.S; ++k) s += inbox[k * cols + c];

@@ -89,12 +89,15 @@ void check_plain(const char* what, const char* name, const Tensor& t, const c10:
     if (t.sizes() != shape) refuse(what, MH3A_ERR_SHAPE, name, " is ", t.sizes(), ": ", shape, " is wanted");
 }
 
+// The stride of a dimension of one element says nothing.
+int64_t stride_of(const Tensor& t, int64_t d) { return t.size(d) > 1 ? t.stride(d) : 0; }
+
 // Whether a tensor starts on a 16-byte boundary with strides of whole 16 bytes (but the last).
 bool aligned16(const Tensor& t) {
     if (reinterpret_cast<uintptr_t>(t.data_ptr()) % 16) return false;
     const int64_t per = 16 / t.element_size();
     for (int64_t i = 0; i + 1 < t.dim(); ++i)
-        if (t.stride(i) % per) return false;
+        if (stride_of(t, i) % per) return false;
     return true;
 }
 bool aligned16(const Opt& t) { return !t || aligned16(*t); }
@@ -157,7 +160,7 @@ std::tuple<Tensor, Tensor, Tensor> group_norm_act(const Tensor& x, int64_t group
         &p, 0, aligned16(x) && aligned16(y) && aligned16(weight) && aligned16(bias) && aligned16(alpha) && aligned16(beta));
     Tensor ws;
     if (n) ws = empty({(int64_t)n}, at::kByte, device);
-    check(mh3a_group_norm_act(&p, x.data_ptr(), x.stride(0), x.stride(1), y.data_ptr(), mean.data_ptr<float>(),
+    check(mh3a_group_norm_act(&p, x.data_ptr(), stride_of(x, 0), stride_of(x, 1), y.data_ptr(), mean.data_ptr<float>(),
                               rstd.data_ptr<float>(), n ? ws.data_ptr() : nullptr, n, on.stream()),
           what);
     on.inputs({&x, opt(weight), opt(bias), opt(alpha), opt(beta), opt(lengths), opt(out)});
@@ -189,7 +192,7 @@ std::tuple<Tensor, Opt, Opt, Opt, Opt> group_norm_act_backward(const Tensor& dy,
         &p, 1, aligned16(x) && aligned16(dy) && aligned16(dx) && aligned16(weight) && aligned16(bias) && aligned16(alpha) && aligned16(beta));
     Tensor ws;
     if (n) ws = empty({(int64_t)n}, at::kByte, device);
-    check(mh3a_group_norm_act_backward(&p, x.data_ptr(), x.stride(0), x.stride(1), dy.data_ptr(), dy.stride(0), dy.stride(1),
+    check(mh3a_group_norm_act_backward(&p, x.data_ptr(), stride_of(x, 0), stride_of(x, 1), dy.data_ptr(), stride_of(dy, 0), stride_of(dy, 1),
                                        mean.data_ptr<float>(), rstd.data_ptr<float>(), dx.data_ptr(), data<float>(grads[0]),
                                        data<float>(grads[1]), data<float>(grads[2]), data<float>(grads[3]), n ? ws.data_ptr() : nullptr, n,
                                        on.stream()),

@@ -9,7 +9,8 @@ results and the scratch memory.  Tensors are CUDA tensors of one device; a call 
 ``stream`` (a torch stream or a cudaStream_t; the device's current stream when None).  Results and
 scratch are allocated on that stream; ordering the caller's own tensors with it stays the caller's
 business, as everywhere in CUDA, but tensors that are still in use there are kept from the allocator
-until the call is done.  Bad arguments raise ``MH3AError`` before anything is launched.
+until the call is done.  Bad arguments raise ``MH3AError`` before anything is launched.  The calls
+record no autograd graph: a gradient is a call of its own.
 """
 from __future__ import annotations
 

@@ -313,7 +313,9 @@ MH3A_API long long mh3a_device_bytes(const mh3a_handle* h);
  * is a matrix product over the B T frames.  None of them needs a handle.  They run on the current
  * device, keep nothing between calls, allocate nothing and take their scratch memory from the
  * caller, so calls with scratch of their own may overlap on any streams, and every call can be
- * captured into a CUDA graph.  Results do not depend on timing: no sum is formed with atomics.
+ * captured into a CUDA graph.  Results do not depend on timing: no sum is formed with atomics.  Every
+ * wait in their kernels has a time limit; a kernel that gave one up (a defect, never an expected
+ * outcome) leaves NaN in the results that depend on it.
  * ------------------------------------------------------------------------------------------- */
 typedef enum { MH3A_DTYPE_F32 = 0, MH3A_DTYPE_F16 = 1, MH3A_DTYPE_BF16 = 2 } mh3a_dtype;
 

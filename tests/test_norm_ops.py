@@ -130,7 +130,9 @@ def test_strided_and_repeated_rows(T, dtype):
     x, w, b, al, be = case(1, 3 * T, 2 * Cn, "silu", dtype, seed=2)
     wide = x.view(3, T, 2 * Cn)
     w, b = w[:Cn].contiguous(), b[:Cn].contiguous()
-    views = [wide[:, :, Cn:], wide.view(T, 3, 2 * Cn).transpose(0, 1)[..., :Cn], wide[:1, :, :Cn].expand(3, T, Cn),
+    odd = torch.empty(3, T * Cn + 1, device="cuda", dtype=wide.dtype)  # an item of one row of a strided batch
+    odd[:1, :T * Cn] = wide[:1, :, :Cn].reshape(1, -1)
+    views = [odd[:1, :T * Cn].unflatten(1, (T, Cn)), wide[:1, :1, :Cn].expand(2, T, Cn), wide[:, :, Cn:], wide.view(T, 3, 2 * Cn).transpose(0, 1)[..., :Cn], wide[:1, :, :Cn].expand(3, T, Cn),
              wide[:, :, 1:Cn + 1]]
     for v in views:
         _, mean, rstd = check_forward(v, G, w, b, "silu", None, None)
