@@ -11,7 +11,9 @@
 // sums of a chunk of rows, their combination in fixed order, then the elementwise pass.  Rows are
 // channels wide, so a warp reads whole rows (512 bytes) and every thread keeps one fixed run of V
 // channels: its statistics stay per channel in registers, and groups of any width, also ones that end
-// inside a vector, are put together only at the end.
+// inside a vector, are put together only at the end.  None of its kernels lets the next one in early:
+// grids that fill every SM once then start on SMs that still hold the blocks before them, and the
+// uneven start costs more (101 against 93 us for sixteen 20 s items) than the launch it hides.
 #include <algorithm>
 
 #include "norm_kernels.cuh"
@@ -155,14 +157,13 @@ __device__ __forceinline__ void unpack_acc(const Pack<T, V>& p, Acc<V>& f) {
     else unpack_pairs<T, V>(p, f.v);
 }
 
-// Per-channel statistics of one chunk of rows.  A thread adds up deviations from the mean of its
-// first rows, so neither a large offset nor an outlier (which moves that mean by a quarter) costs
-// accuracy; threads, warps and chunks are merged as (mean, squared deviations).
+// Statistics of one chunk of rows, per group.  A thread adds up deviations per channel from the mean of
+// its first rows, so neither a large offset nor an outlier (which moves that mean by a quarter) costs
+// accuracy; threads, warps, channels and chunks are merged as (mean, squared deviations).
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 4) k_norm_partial(const NormArgs a) {
     constexpr int H = Acc<V>::H;
     ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
     const Place p = place<V>(a, blockIdx.x);
     const int n = valid_rows(a, p.b);
     const int r0 = min(p.ch * a.rows, n), r1 = min(r0 + a.rows, n);
@@ -233,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_partial(const NormArgs a) 
     for (int i = 0; i < V; ++i) sm[warp][lane * V + i] = st[i];
     __syncthreads();
     if (warp == 0 && lane < a.tx && p.live) {
-        float4* out = reinterpret_cast<float4*>(a.ws) + ((long long)p.b * a.chunks + p.ch) * a.C + p.c;
         for (int w = 1; w < kThreads / 32; ++w) {
             const float nb = sn[w][lane];
             const float f = nb > 0.f ? nb / (cnt + nb) : 0.f;
@@ -242,58 +242,92 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_partial(const NormArgs a) 
             cnt += nb;
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = make_float4(st[i].hi, st[i].lo, st[i].m2, 0.f);
+        for (int i = 0; i < V; ++i) sm[0][lane * V + i] = st[i];
+    }
+    __syncthreads();
+    // The tile's channels of each group it meets.  A group that two tiles share has an entry in each:
+    // entry g + tile, since the next tile begins with this tile's last group or the one after.
+    const int wide = a.tx * V, tile = blockIdx.x / a.chunks % a.ctiles;
+    const int c0 = tile * wide, c1 = min(a.C, c0 + wide);
+    const double n_rows = r1 - r0;
+    float4* out = reinterpret_cast<float4*>(a.ws) + ((long long)p.b * a.chunks + p.ch) * (a.G + a.ctiles) + tile;
+    const int g0 = c0 / a.D, g1 = (c1 - 1) / a.D;
+    // sums about the first channel's mean, in fp64: no second pass, and nothing to lose but its distance
+    // from the group's mean, squared, in 53 bits
+    auto add_channel = [&](const Stat& v, const Stat& ref, double& s0, double& q0) {
+        const double d = (double)(v.hi - ref.hi) + (double)(v.lo - ref.lo);
+        s0 += d;
+        q0 += fma(d * n_rows, d, (double)v.m2);
+    };
+    auto put = [&](int g, const Stat& ref, double s0, double q0, int channels) {
+        const double d = s0 / channels, mean = (double)ref.hi + (double)ref.lo + d;
+        const float hi = (float)mean;
+        out[g] = make_float4(hi, (float)(mean - hi), (float)(q0 - n_rows * s0 * d), (float)(n_rows * channels));
+    };
+    if (a.D <= 32) {  // a thread a group
+        for (int g = g0 + threadIdx.x; g <= g1; g += kThreads) {
+            const int first = max(g * a.D, c0), last = min((g + 1) * a.D, c1);
+            const Stat ref = sm[0][first - c0];
+            double s0 = 0.0, q0 = 0.0;
+            for (int c = first; c < last; ++c) add_channel(sm[0][c - c0], ref, s0, q0);
+            put(g, ref, s0, q0, last - first);
+        }
+    } else {  // a warp a group
+        for (int g = g0 + warp; g <= g1; g += kThreads / 32) {
+            const int first = max(g * a.D, c0), last = min((g + 1) * a.D, c1);
+            const Stat ref = sm[0][first - c0];
+            double s0 = 0.0, q0 = 0.0;
+            for (int c = first + lane; c < last; c += 32) add_channel(sm[0][c - c0], ref, s0, q0);
+            s0 = warp_sum(s0);
+            q0 = warp_sum(q0);
+            if (lane == 0) put(g, ref, s0, q0, last - first);
+        }
     }
 }
 
-constexpr int kStatThreads = 512;
+constexpr int kStatThreads = 128;
 
-__device__ __forceinline__ double block_sum(double v, double* sh) {
-#pragma unroll
-    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double s = 0;
-#pragma unroll
-    for (int w = 0; w < kStatThreads / 32; ++w) s += sh[w];
-    return s;
-}
-
-// mean and rstd of one (item, group) from the chunks' statistics, in fp64.  `tx` threads (a power of
-// two) stand along the group's channels, the others along the chunks.
-__global__ void __launch_bounds__(kStatThreads) k_norm_stats(const NormArgs a, int tx) {
+// mean and rstd of one (item, group) from the entries of its chunks and channel tiles (of `wide`
+// channels), in fp64.  `tx` threads (a power of two) stand along the tiles, the others along the chunks.
+__global__ void __launch_bounds__(kStatThreads) k_norm_stats(const NormArgs a, int wide, int tx) {
     ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    __shared__ double sh[kStatThreads / 32];
+    __shared__ double sh[2][kStatThreads / 32];
     const int b = blockIdx.x / a.G, g = blockIdx.x % a.G;
     const int n = valid_rows(a, b);
-    const float4* part = reinterpret_cast<const float4*>(a.ws) + (long long)b * a.chunks * a.C + (long long)g * a.D;
+    const float4* part = reinterpret_cast<const float4*>(a.ws) + (long long)b * a.chunks * (a.G + a.ctiles) + g;
     const int used = (n + a.rows - 1) / a.rows;
+    const int t0 = (int)((long long)g * a.D / wide), t1 = (int)((((long long)g + 1) * a.D - 1) / wide);
+    const long long step = a.G + a.ctiles;
     const int lx = threadIdx.x & (tx - 1), ly = threadIdx.x / tx, ny = kStatThreads / tx;
-    double s = 0;
-    for (int c = lx; c < a.D; c += tx) {
+    // about the first entry's mean, as in k_norm_partial
+    const float4 first = n > 0 ? part[t0] : make_float4(0.f, 0.f, 0.f, 0.f);
+    const double ref = (double)first.x + (double)first.y;
+    double s = 0, q = 0;
+    for (int t = t0 + lx; t <= t1; t += tx) {
 #pragma unroll 4
         for (int ch = ly; ch < used; ch += ny) {
-            const float4 v = part[(long long)ch * a.C + c];
-            s += ((double)v.x + (double)v.y) * min(a.rows, n - ch * a.rows);
+            const float4 v = part[ch * step + t];
+            const double d = (double)v.x + (double)v.y - ref;
+            s += d * v.w;
+            q += fma(d * v.w, d, (double)v.z);
         }
     }
-    const double inv = n > 0 ? 1.0 / ((double)n * a.D) : 0.0;
-    const double mean = block_sum(s, sh) * inv;
-    double q = 0;
-    for (int c = lx; c < a.D; c += tx) {
-#pragma unroll 4
-        for (int ch = ly; ch < used; ch += ny) {
-            const float4 v = part[(long long)ch * a.C + c];
-            const double d = (double)v.x + (double)v.y - mean;
-            q += (double)v.z + d * d * min(a.rows, n - ch * a.rows);
-        }
+    s = warp_sum(s);
+    q = warp_sum(q);
+    if ((threadIdx.x & 31) == 0) {
+        sh[0][threadIdx.x >> 5] = s;
+        sh[1][threadIdx.x >> 5] = q;
     }
-    const double var = block_sum(q, sh) * inv;
+    __syncthreads();
     if (threadIdx.x == 0) {
-        a.mean[blockIdx.x] = (float)mean;
-        a.rstd[blockIdx.x] = 1.0f / sqrtf((float)(var + (double)a.eps));
+        for (int w = 1; w < kStatThreads / 32; ++w) {
+            s += sh[0][w];
+            q += sh[1][w];
+        }
+        const double inv = n > 0 ? 1.0 / ((double)n * a.D) : 0.0, d = s * inv;
+        const double var = q * inv - d * d;
+        a.mean[blockIdx.x] = (float)(ref + d);
+        a.rstd[blockIdx.x] = 1.0f / sqrtf((float)((var > 0.0 ? var : var == var ? 0.0 : var) + (double)a.eps));
     }
 }
 
@@ -387,7 +421,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_bwd_partial(const NormArgs
     constexpr bool kPrecise = sizeof(T) == 4;
     constexpr int NS = kSums<ACT>, H = Acc<V>::H;
     ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
     const Place p = place<V>(a, blockIdx.x);
     const int n = valid_rows(a, p.b);
     const int r0 = min(p.ch * a.rows, n), r1 = min(r0 + a.rows, n);
@@ -677,7 +710,7 @@ bool go_resident(const NormArgs& a, const Resident& r, cudaStream_t s) {
 size_t general_bytes(NormArgs a, int act, int backward, int V) {
     plan_general(&a, V, backward ? kBwdPerSm : kFwdPerSm);
     const long long ns = act == MH3A_ACT_SNAKE_BETA ? 4 : 2;
-    long long floats = (long long)a.B * a.chunks * a.C * (backward ? ns : 4);
+    long long floats = (long long)a.B * a.chunks * (backward ? a.C * ns : (a.G + a.ctiles) * 4LL);
     if (backward) floats += ((long long)a.B * a.C * ns + 3) / 4 * 4 + 2LL * a.B * a.G;
     return ((size_t)floats * 4 + 255) / 256 * 256;
 }
@@ -723,7 +756,7 @@ template <typename T, int V>
 bool forward_general(const NormArgs& a, int act, cudaStream_t s) {
     const long long grid = grid_general(a);
     if (!go(k_norm_partial<T, V>, grid, kThreads, s, a)) return false;
-    if (!go(k_norm_stats, (long long)a.B * a.G, kStatThreads, s, a, pow2_ceil(a.D, kStatThreads))) return false;
+    if (!go(k_norm_stats, (long long)a.B * a.G, kStatThreads, s, a, a.tx * V, pow2_ceil(a.tx * V % a.D ? (a.D - 1) / (a.tx * V) + 2 : 1, kStatThreads))) return false;
     switch (act) {
         case MH3A_ACT_SILU: return go(k_norm_apply<T, V, MH3A_ACT_SILU>, grid, kThreads, s, a);
         case MH3A_ACT_SNAKE_BETA: return go(k_norm_apply<T, V, MH3A_ACT_SNAKE_BETA>, grid, kThreads, s, a);
