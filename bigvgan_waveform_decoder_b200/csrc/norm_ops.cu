@@ -15,6 +15,7 @@
 // grids that fill every SM once then start on SMs that still hold the blocks before them, and the
 // uneven start costs more (101 against 93 us for sixteen 20 s items) than the launch it hides.
 #include <algorithm>
+#include <initializer_list>
 
 #include "norm_kernels.cuh"
 #include "norm_resident.cuh"
@@ -706,6 +707,10 @@ bool go_resident(const NormArgs& a, const Resident& r, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, Kern, a, r) == cudaSuccess;
 }
 
+// Vectors of the general form.  Backward takes 8 bytes at most of 16-bit types: twice as many channels'
+// sums and parameters would halve the blocks an SM holds.
+int general_width(int V, int backward) { return backward ? std::min(V, 4) : V; }
+
 // Scratch of the general form with vectors of V channels.
 size_t general_bytes(NormArgs a, int act, int backward, int V) {
     plan_general(&a, V, backward ? kBwdPerSm : kFwdPerSm);
@@ -715,7 +720,8 @@ size_t general_bytes(NormArgs a, int act, int backward, int V) {
     return ((size_t)floats * 4 + 255) / 256 * 256;
 }
 
-// The way a call goes, by its sizes and whether everything is aligned to whole vectors.
+// The way a call goes, by its sizes, the vectors of V channels that its pointers and strides allow, and
+// whether the parameters are aligned to 16 bytes.
 struct Way {
     bool resident;
     Resident r;
@@ -723,22 +729,21 @@ struct Way {
 };
 
 template <typename T>
-Way way(const NormArgs& a, int act, int backward, bool vec) {
-    constexpr int V = 16 / sizeof(T);
+Way way(const NormArgs& a, int act, int backward, int V, bool params) {
     Way w{};
     const int ns = act == MH3A_ACT_SNAKE_BETA ? 4 : 2;
     auto extra = [&](int W, int S) { return backward ? res_bwd_extra(W, a.D, V, S, ns) : res_fwd_extra(W, a.D, V, S); };
-    w.resident = vec && plan_resident(a, V, sizeof(T), (backward ? 2 : 1) * sizeof(T), extra, &w.r);
+    w.resident = V == 16 / (int)sizeof(T) && params && plan_resident(a, V, sizeof(T), (backward ? 2 : 1) * sizeof(T), extra, &w.r);
     if (w.resident) w.bytes = backward && a.B > 1 ? ((size_t)a.B * a.C * ns * 4 + 255) / 256 * 256 : 0;
-    else w.bytes = general_bytes(a, act, backward, !vec ? 1 : backward ? 4 : V);
+    else w.bytes = general_bytes(a, act, backward, general_width(V, backward));
     return w;
 }
 
-Way way(const NormArgs& a, int dtype, int act, int backward, bool vec) {
+Way way(const NormArgs& a, int dtype, int act, int backward, int V, bool params) {
     switch (dtype) {
-        case MH3A_DTYPE_F32: return way<float>(a, act, backward, vec);
-        case MH3A_DTYPE_F16: return way<__half>(a, act, backward, vec);
-        default: return way<__nv_bfloat16>(a, act, backward, vec);
+        case MH3A_DTYPE_F32: return way<float>(a, act, backward, V, params);
+        case MH3A_DTYPE_F16: return way<__half>(a, act, backward, V, params);
+        default: return way<__nv_bfloat16>(a, act, backward, V, params);
     }
 }
 
@@ -765,7 +770,7 @@ bool forward_general(const NormArgs& a, int act, cudaStream_t s) {
 }
 
 template <typename T>
-bool forward(NormArgs& a, const Way& w, int act, bool vec, cudaStream_t s) {
+bool forward(NormArgs& a, const Way& w, int act, int width, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
     if (w.resident) {
         switch (act) {
@@ -774,8 +779,12 @@ bool forward(NormArgs& a, const Way& w, int act, bool vec, cudaStream_t s) {
             default: return forward_resident<T, V, MH3A_ACT_NONE>(a, w.r, s);
         }
     }
-    plan_general(&a, vec ? V : 1, kFwdPerSm);
-    return vec ? forward_general<T, V>(a, act, s) : forward_general<T, 1>(a, act, s);
+    plan_general(&a, general_width(width, 0), kFwdPerSm);
+    if constexpr (V == 8) {
+        if (width == 8) return forward_general<T, 8>(a, act, s);
+    }
+    if (width == 4) return forward_general<T, 4>(a, act, s);
+    return width == 2 ? forward_general<T, 2>(a, act, s) : forward_general<T, 1>(a, act, s);
 }
 
 template <typename T, int V, int ACT>
@@ -793,7 +802,7 @@ bool backward_general(const NormArgs& a, cudaStream_t s) {
 }
 
 template <typename T, int ACT>
-bool backward_act(NormArgs& a, const Way& w, bool vec, cudaStream_t s) {
+bool backward_act(NormArgs& a, const Way& w, int width, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T), NS = kSums<ACT>;
     if (w.resident) {
         const bool ok = a.D % V == 0 ? go_resident<k_norm_bwd_resident<T, V, ACT, true>>(a, w.r, s)
@@ -801,18 +810,18 @@ bool backward_act(NormArgs& a, const Way& w, bool vec, cudaStream_t s) {
         if (!ok || a.B == 1) return ok;
         return go(k_norm_bwd_final, (a.C + 255LL) / 256, 256, s, a, (const float*)a.ws, (float2*)nullptr, NS, 0);
     }
-    // 8-byte vectors for 16-bit types: twice as many channels' sums and parameters would halve the blocks
-    // an SM holds
-    plan_general(&a, vec ? 4 : 1, kBwdPerSm);
-    return vec ? backward_general<T, 4, ACT>(a, s) : backward_general<T, 1, ACT>(a, s);
+    width = general_width(width, 1);
+    plan_general(&a, width, kBwdPerSm);
+    if (width == 4) return backward_general<T, 4, ACT>(a, s);
+    return width == 2 ? backward_general<T, 2, ACT>(a, s) : backward_general<T, 1, ACT>(a, s);
 }
 
 template <typename T>
-bool backward(NormArgs& a, const Way& w, int act, bool vec, cudaStream_t s) {
+bool backward(NormArgs& a, const Way& w, int act, int width, cudaStream_t s) {
     switch (act) {
-        case MH3A_ACT_SILU: return backward_act<T, MH3A_ACT_SILU>(a, w, vec, s);
-        case MH3A_ACT_SNAKE_BETA: return backward_act<T, MH3A_ACT_SNAKE_BETA>(a, w, vec, s);
-        default: return backward_act<T, MH3A_ACT_NONE>(a, w, vec, s);
+        case MH3A_ACT_SILU: return backward_act<T, MH3A_ACT_SILU>(a, w, width, s);
+        case MH3A_ACT_SNAKE_BETA: return backward_act<T, MH3A_ACT_SNAKE_BETA>(a, w, width, s);
+        default: return backward_act<T, MH3A_ACT_NONE>(a, w, width, s);
     }
 }
 
@@ -846,12 +855,24 @@ NormArgs base_args(const mh3a_norm* p) {
     return a;
 }
 
-// Whether whole vectors can be used: parameters are then read by 16-byte loads.
 bool params_fit(const NormArgs& a) {
     return aligned(a.weight, 16) && aligned(a.bias, 16) && aligned(a.alpha, 16) && aligned(a.beta, 16);
 }
 
-bool strides_fit(long long b, long long r, int V) { return b % V == 0 && r % V == 0; }
+// The widest vectors (16 bytes at most) that the channels, the pointers and the strides allow.
+int vector_width(const NormArgs& a, int e, std::initializer_list<const void*> pointers, std::initializer_list<long long> strides) {
+    int V = 16 / e;
+    auto fits = [&]() {
+        if (a.C % V) return false;
+        for (const void* p : pointers)
+            if (!aligned(p, (size_t)V * e)) return false;
+        for (long long s : strides)
+            if (s % V) return false;
+        return true;
+    };
+    while (V > 1 && !fits()) V /= 2;
+    return V;
+}
 
 }  // namespace norm
 }  // namespace mh3a
@@ -862,10 +883,11 @@ using namespace mh3a::norm;
 extern "C" MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward, int aligned_all) {
     if (check(p) != MH3A_OK) return 0;
     const NormArgs a = base_args(p);
-    const size_t any = way(a, p->dtype, p->act, backward, false).bytes;
-    const bool vec = p->C % (16 / elem_bytes(p->dtype)) == 0;
-    const size_t whole = vec ? way(a, p->dtype, p->act, backward, true).bytes : any;
-    return aligned_all ? whole : std::max(any, whole);
+    const int e = elem_bytes(p->dtype), V = vector_width(a, e, {}, {});
+    size_t most = way(a, p->dtype, p->act, backward, V, true).bytes;
+    if (!aligned_all)
+        for (int v = V; v >= 1; v /= 2) most = std::max(most, way(a, p->dtype, p->act, backward, v, false).bytes);
+    return most;
 }
 
 extern "C" MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const void* x, long long x_batch_stride,
@@ -874,7 +896,7 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const vo
     const mh3a_status st = check(p);
     if (st != MH3A_OK) return st;
     if (!x || !y || !mean || !rstd || x_batch_stride < 0 || x_row_stride < 0) return MH3A_ERR_INVALID_ARG;
-    const int e = elem_bytes(p->dtype), V = 16 / e;
+    const int e = elem_bytes(p->dtype);
     if (!aligned(x, e) || !aligned(y, e) || !aligned(mean, 4) || !aligned(rstd, 4)) return MH3A_ERR_INVALID_ARG;
     NormArgs a = base_args(p);
     a.x = x;
@@ -884,15 +906,15 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const vo
     a.mean = mean;
     a.rstd = rstd;
     a.ws = static_cast<float*>(workspace);
-    const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(y, 16) && strides_fit(a.xb, a.xr, V) && params_fit(a);
-    const Way w = way(a, p->dtype, p->act, 0, vec);
+    const int V = vector_width(a, e, {x, y}, {a.xb, a.xr});
+    const Way w = way(a, p->dtype, p->act, 0, V, params_fit(a));
     if (!scratch_ok(workspace, workspace_bytes, w.bytes)) return MH3A_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     bool ok;
     switch (p->dtype) {
-        case MH3A_DTYPE_F32: ok = forward<float>(a, w, p->act, vec, s); break;
-        case MH3A_DTYPE_F16: ok = forward<__half>(a, w, p->act, vec, s); break;
-        default: ok = forward<__nv_bfloat16>(a, w, p->act, vec, s);
+        case MH3A_DTYPE_F32: ok = forward<float>(a, w, p->act, V, s); break;
+        case MH3A_DTYPE_F16: ok = forward<__half>(a, w, p->act, V, s); break;
+        default: ok = forward<__nv_bfloat16>(a, w, p->act, V, s);
     }
     return ok ? MH3A_OK : launch_failed("mh3a_group_norm_act");
 }
@@ -908,7 +930,7 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p,
     if (!x || !dy || !dx || !mean || !rstd) return MH3A_ERR_INVALID_ARG;
     if (x_batch_stride < 0 || x_row_stride < 0 || dy_batch_stride < 0 || dy_row_stride < 0) return MH3A_ERR_INVALID_ARG;
     if (p->act != MH3A_ACT_SNAKE_BETA && (dalpha || dbeta)) return MH3A_ERR_INVALID_ARG;
-    const int e = elem_bytes(p->dtype), V = 16 / e;
+    const int e = elem_bytes(p->dtype);
     if (!aligned(x, e) || !aligned(dy, e) || !aligned(dx, e)) return MH3A_ERR_INVALID_ARG;
     NormArgs a = base_args(p);
     a.x = x;
@@ -925,16 +947,15 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p,
     a.dalpha = dalpha;
     a.dbeta = dbeta;
     a.ws = static_cast<float*>(workspace);
-    const bool vec = p->C % V == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(dx, 16) &&
-                     strides_fit(a.xb, a.xr, V) && strides_fit(a.gb, a.gr, V) && params_fit(a);
-    const Way w = way(a, p->dtype, p->act, 1, vec);
+    const int V = vector_width(a, e, {x, dy, dx}, {a.xb, a.xr, a.gb, a.gr});
+    const Way w = way(a, p->dtype, p->act, 1, V, params_fit(a));
     if (!scratch_ok(workspace, workspace_bytes, w.bytes)) return MH3A_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     bool ok;
     switch (p->dtype) {
-        case MH3A_DTYPE_F32: ok = backward<float>(a, w, p->act, vec, s); break;
-        case MH3A_DTYPE_F16: ok = backward<__half>(a, w, p->act, vec, s); break;
-        default: ok = backward<__nv_bfloat16>(a, w, p->act, vec, s);
+        case MH3A_DTYPE_F32: ok = backward<float>(a, w, p->act, V, s); break;
+        case MH3A_DTYPE_F16: ok = backward<__half>(a, w, p->act, V, s); break;
+        default: ok = backward<__nv_bfloat16>(a, w, p->act, V, s);
     }
     return ok ? MH3A_OK : launch_failed("mh3a_group_norm_act_backward");
 }

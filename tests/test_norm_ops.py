@@ -76,6 +76,8 @@ SHAPES = [
     (1, 5, 2048, 32),
     (2, 33, 25, 5),       # odd width: no vector access
     (1, 300, 7, 7),
+    (2, 90, 174, 3),      # even: pairs
+    (2, 6000, 30, 2),
     (2, 500, 200, 8),     # groups that end inside a vector
     (2, 130, 12, 4),      # 16-bit rows that are no multiple of 16 bytes
     (2, 2000, 512, 32),
