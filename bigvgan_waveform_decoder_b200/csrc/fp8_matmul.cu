@@ -402,7 +402,7 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                 } else {
                     // Column scales: a lane of the fragments needs a quarter of them, where a lane that holds a
                     // whole row would read all from shared memory, 512 bytes a load and four columns (74 us
-                    // against 66 at 2048 x 2048 x 6400).
+                    // against 66 at 2048 x 2048 x 6400 in tiles of 128 columns).
                     uint32_t v[2][2][kLd / 2];
                     auto load = [&](int c) {
                         tmem_ld_frag(buf + c * kLd, v[c & 1][0]);
@@ -505,14 +505,18 @@ int launch(const MatmulArgs& m, cudaStream_t s) {
 
 template <typename O, bool WIDE>
 int launch_nt(const MatmulArgs& m, cudaStream_t s) {
-    // The widest tile that still gives every SM one; narrower ones read the operands more often.
+    // Rounds of tiles over the SMs, times what a round takes with tiles of that width (relative, from
+    // K = 2048: 8.5, 5.6, 4.1, 3.4 and 3.0 us).  Measured there, us with 256 / 128 / 64 / 32 / 16 columns:
+    // 64 x 2048: 11.1 / 8.0 / 6.8 / 6.3 / 5.9; 800 x 1024: 11.7 / 8.6 / 7.2 / 10.6 / 17.6; 800 x 2048: 12.0 /
+    // 9.2 / 12.0 / 18.8 / 29.6; 2048 x 2048: 12.9 / 16.0 / 21.9 / 31.7 / 57.5.
     const long long mt = (m.M + kM - 1LL) / kM;
-    auto tiles = [&](int nt) { return mt * ((m.N + nt - 1LL) / nt); };
-    if (tiles(256) >= kSms) return launch<O, 256, WIDE>(m, s);
-    if (tiles(128) >= kSms) return launch<O, 128, WIDE>(m, s);
-    if (tiles(64) >= kSms / 2) return launch<O, 64, WIDE>(m, s);
-    if (tiles(32) >= kSms / 2) return launch<O, 32, WIDE>(m, s);
-    return launch<O, 16, WIDE>(m, s);
+    auto cost = [&](int nt, long long round) { return (mt * ((m.N + nt - 1LL) / nt) + kSms - 1) / kSms * round; };
+    const long long c256 = cost(256, 17), c128 = cost(128, 11), c64 = cost(64, 8), c32 = cost(32, 7), c16 = cost(16, 6);
+    const long long least = std::min({c256, c128, c64, c32, c16});
+    if (c256 == least) return launch<O, 256, WIDE>(m, s);
+    if (c128 == least) return launch<O, 128, WIDE>(m, s);
+    if (c64 == least) return launch<O, 64, WIDE>(m, s);
+    return c32 == least ? launch<O, 32, WIDE>(m, s) : launch<O, 16, WIDE>(m, s);
 }
 
 template <typename O>

@@ -506,8 +506,11 @@ __global__ void __launch_bounds__(256) k_norm_bwd_sum(const NormArgs a, float* s
     const int n = valid_rows(a, b);
     const int used = (n + a.rows - 1) / a.rows;
     double s = 0;
-    if (j < width)
-        for (int ch = row; ch < used; ch += 8) s += a.ws[((long long)b * a.chunks + ch) * width + j];
+    if (j < width) {
+        const float* from = a.ws + (long long)b * a.chunks * width + j;
+#pragma unroll 8
+        for (int ch = row; ch < used; ch += 8) s += from[ch * width];
+    }
     sh[row][lane] = s;
     __syncthreads();
     if (row == 0 && j < width) {
@@ -516,16 +519,18 @@ __global__ void __launch_bounds__(256) k_norm_bwd_sum(const NormArgs a, float* s
     }
 }
 
-// Warps [0, B G): the two group means of dx; blocks behind them: parameter gradients.
+// The first `group_blocks` blocks: the two group means of dx, a warp an (item, group).  Blocks behind
+// them: parameter gradients, the items' sums in fixed order, 32 x 8 threads, one column of sums each.
 __global__ void __launch_bounds__(256) k_norm_bwd_final(const NormArgs a, const float* sums, float2* means, int ns,
                                                         int group_blocks) {
     ptx::grid_dep_wait();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     if ((int)blockIdx.x < group_blocks) {
-        const long long bg = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+        const long long bg = (long long)blockIdx.x * 8 + row;
         if (bg >= (long long)a.B * a.G) return;
         const int b = (int)(bg / a.G), g = (int)(bg % a.G);
         double s1 = 0, s2 = 0;
+#pragma unroll 4
         for (int c = lane; c < a.D; c += 32) {
             const long long ch = (long long)g * a.D + c;
             const double w = a.weight ? (double)__ldg(a.weight + ch) : 1.0;
@@ -533,11 +538,8 @@ __global__ void __launch_bounds__(256) k_norm_bwd_final(const NormArgs a, const 
             s1 += w * s[0];
             s2 += w * s[1];
         }
-#pragma unroll
-        for (int off = 16; off; off >>= 1) {
-            s1 += __shfl_xor_sync(0xffffffffu, s1, off);
-            s2 += __shfl_xor_sync(0xffffffffu, s2, off);
-        }
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
         if (lane == 0) {
             const int n = valid_rows(a, b);
             const double inv = n > 0 ? 1.0 / ((double)n * a.D) : 0.0;
@@ -545,18 +547,25 @@ __global__ void __launch_bounds__(256) k_norm_bwd_final(const NormArgs a, const 
         }
         return;
     }
-    const long long c = (long long)(blockIdx.x - group_blocks) * 256 + threadIdx.x;
-    if (c >= a.C) return;
-    double s[4] = {0, 0, 0, 0};
-    for (int b = 0; b < a.B; ++b)
-        for (int j = 0; j < ns; ++j) s[j] += sums[((long long)b * a.C + c) * ns + j];
-    if (a.dbias) a.dbias[c] = (float)s[0];
-    if (a.dweight) a.dweight[c] = (float)s[1];
-    if (a.dalpha) a.dalpha[c] = (float)s[2];
-    if (a.dbeta) {
-        const double ib = 1.0 / (double)(a.beta[c] + 1e-9f);
-        a.dbeta[c] = (float)(-s[3] * ib * ib);
+    __shared__ double sh[8][33];
+    const long long width = (long long)a.C * ns, j = (long long)(blockIdx.x - group_blocks) * 32 + lane;
+    double s = 0;
+    if (j < width) {
+#pragma unroll 4
+        for (int b = row; b < a.B; b += 8) s += sums[b * width + j];
     }
+    sh[row][lane] = s;
+    __syncthreads();
+    if (row != 0 || j >= width) return;
+    for (int r = 1; r < 8; ++r) s += sh[r][lane];
+    const int c = (int)(j / ns), k = (int)(j % ns);
+    float* const out = k == 0 ? a.dbias : k == 1 ? a.dweight : k == 2 ? a.dalpha : a.dbeta;
+    if (!out) return;
+    if (k == 3) {
+        const double ib = 1.0 / (double)(a.beta[c] + 1e-9f);
+        s = -s * ib * ib;
+    }
+    out[c] = (float)s;
 }
 
 // dx, from the tensor's end as in k_norm_apply.
@@ -797,7 +806,7 @@ bool backward_general(const NormArgs& a, cudaStream_t s) {
     const int tiles = (int)(((long long)a.C * NS + 31) / 32);
     if (!go(k_norm_bwd_sum, (long long)a.B * tiles, 256, s, a, sums, NS, tiles)) return false;
     const int gblocks = (int)(((long long)a.B * a.G + 7) / 8);
-    if (!go(k_norm_bwd_final, gblocks + (a.C + 255LL) / 256, 256, s, a, (const float*)sums, means, NS, gblocks)) return false;
+    if (!go(k_norm_bwd_final, gblocks + tiles, 256, s, a, (const float*)sums, means, NS, gblocks)) return false;
     return go(k_norm_bwd_apply<T, V, ACT>, grid, kThreads, s, a, (const float2*)means);
 }
 
@@ -808,7 +817,7 @@ bool backward_act(NormArgs& a, const Way& w, int width, cudaStream_t s) {
         const bool ok = a.D % V == 0 ? go_resident<k_norm_bwd_resident<T, V, ACT, true>>(a, w.r, s)
                                      : go_resident<k_norm_bwd_resident<T, V, ACT, false>>(a, w.r, s);
         if (!ok || a.B == 1) return ok;
-        return go(k_norm_bwd_final, (a.C + 255LL) / 256, 256, s, a, (const float*)a.ws, (float2*)nullptr, NS, 0);
+        return go(k_norm_bwd_final, ((long long)a.C * NS + 31) / 32, 256, s, a, (const float*)a.ws, (float2*)nullptr, NS, 0);
     }
     width = general_width(width, 1);
     plan_general(&a, width, kBwdPerSm);
