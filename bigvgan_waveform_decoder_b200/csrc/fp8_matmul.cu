@@ -26,8 +26,6 @@ namespace fp8 {
 namespace {
 
 constexpr int kM = 128;     // tile rows (tensor-memory lanes)
-constexpr int kScaleSlots = 4;  // steps whose column scales are held or on their way
-constexpr int kAhead = 3;       // steps that row scales (and those of wide blocks) are fetched ahead
 constexpr int kPitch = 80;  // staging row of 64 bytes: 16-byte accesses of 8 rows meet no bank twice
 
 struct MatmulParams {
@@ -46,8 +44,13 @@ struct Cfg {
     static constexpr int EW = NT >= 128 ? 8 : 4;          // epilogue warps
     static constexpr int CW = NT / (EW / 4);              // columns of an epilogue warp
     static constexpr int kThreads = 128 + 32 * EW;
-    static constexpr int kAcc = NT == 256 ? 2 : 4;        // tensor-memory buffers
-    static constexpr int kCols = kAcc * NT < 32 ? 32 : kAcc * NT;
+    // Steps of K between two handshakes of the tensor core and the epilogue, each with columns of its own:
+    // a wait costs as much as adding up a narrow tile.
+    static constexpr int kStep = NT == 256 ? 1 : NT == 128 ? 2 : 4;
+    static constexpr int kAcc = std::min(4, 512 / (kStep * NT));  // tensor-memory buffers
+    static constexpr int kCols = kAcc * kStep * NT;
+    static constexpr int kAhead = kStep == 1 ? 3 : 2 * kStep;  // steps that scales are fetched ahead
+    static constexpr int kScaleSlots = kStep == 1 ? 4 : 2 * kStep;
     static constexpr int kStageBytes = (kM + NT) * kBlock;
     static constexpr int kStaging = EW * 32 * kPitch;
     static constexpr int kOther = kStaging + kScaleSlots * NT * 4 + 1024 + 512;
@@ -189,19 +192,20 @@ __device__ __forceinline__ void write_out(const MatmulParams& p, const float2 (&
             }
         }
         __syncwarp();
+        if (p.vec_out && n0 + c0 + kStep <= p.N) {
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-            const int at = k * 32 + lane, row = at / kVecs, v = at % kVecs;
-            const int n = n0 + c0 + v * (int)(16 / sizeof(O)), left = p.N - n;
-            if (m0 + row < p.M && left > 0) {
-                const unsigned char* from = stage + row * kPitch + v * 16;
-                O* dst = out + (long long)(m0 + row) * p.os + n;
-                if (p.vec_out && left >= (int)(16 / sizeof(O))) {
-                    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(from);
-                } else {
-                    for (int i = 0; i < min(left, (int)(16 / sizeof(O))); ++i) dst[i] = reinterpret_cast<const O*>(from)[i];
-                }
+            for (int k = 0; k < kVecs; ++k) {
+                const int at = k * 32 + lane, row = at / kVecs, v = at % kVecs;
+                if (m0 + row < p.M)
+                    *reinterpret_cast<uint4*>(out + (long long)(m0 + row) * p.os + n0 + c0 + v * (int)(16 / sizeof(O))) =
+                        *reinterpret_cast<const uint4*>(stage + row * kPitch + v * 16);
             }
+        } else {  // rows that do not start on 16 bytes, the matrix's edge: neighbouring lanes, neighbouring elements
+            const int col = lane % kStep;
+#pragma unroll 4
+            for (int row = lane / kStep; row < 32; row += 32 / kStep)
+                if (m0 + row < p.M && n0 + c0 + col < p.N)
+                    out[(long long)(m0 + row) * p.os + n0 + c0 + col] = reinterpret_cast<const O*>(stage + row * kPitch)[col];
         }
         __syncwarp();
     }
@@ -212,6 +216,7 @@ template <typename O, int NT, bool WIDE>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
 k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
     using C = Cfg<NT>;
+    constexpr int kStep = C::kStep, kAhead = C::kAhead, kScaleSlots = C::kScaleSlots;
     extern __shared__ unsigned char raw[];
     unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     unsigned char* staging = tiles + C::kStages * C::kStageBytes;
@@ -276,21 +281,25 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                 for (int j = max(0, it - C::kStages); j < it; ++j) ptx::mbar_wait(full + j % C::kStages, (j / C::kStages) & 1);
         } else if (warp == 1) {
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);  // e4m3, fp32 sums
-            int it = 0;
+            int it = 0, round = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
-                for (int kb = 0; kb < p.KB && ok; ++kb, ++it) {
-                    const int s = it % C::kStages, b = it % C::kAcc;
-                    if (it >= C::kAcc) ok = ptx::mbar_wait(freed + b, ((it / C::kAcc) & 1) ^ 1);
-                    ok = ok && ptx::mbar_wait(full + s, (it / C::kStages) & 1);
+                for (int k0 = 0; k0 < p.KB && ok; k0 += kStep, ++round) {
+                    const int b = round % C::kAcc, steps = kStep == 1 ? 1 : min(kStep, p.KB - k0), it0 = it;
+                    if (round >= C::kAcc) ok = ptx::mbar_wait(freed + b, ((round / C::kAcc) & 1) ^ 1);
+                    for (int j = 0; j < steps && ok; ++j, ++it) {
+                        const int s = it % C::kStages;
+                        ok = ptx::mbar_wait(full + s, (it / C::kStages) & 1);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint32_t at = ptx::smem_u32(tiles + s * C::kStageBytes);
+                        mma_block_elect(tmem + (b * kStep + j) * NT, desc_sw128(at), desc_sw128(at + kM * kBlock), idesc);
+                        ptx::mma_commit_elect(empty + s);
+                    }
                     if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t at = ptx::smem_u32(tiles + s * C::kStageBytes);
-                    mma_block_elect(tmem + b * NT, desc_sw128(at), desc_sw128(at + kM * kBlock), idesc);
-                    ptx::mma_commit_elect(empty + s);
                     ptx::mma_commit_elect(done + b);
                     if (!WIDE) {
-                        ok = ptx::mbar_wait(sfull + it % kScaleSlots, (it / kScaleSlots) & 1);
+                        for (int i = it0; i < it; ++i) ok = ok && ptx::mbar_wait(sfull + i % kScaleSlots, (i / kScaleSlots) & 1);
                         if (lane == 0) ptx::mbar_arrive(done + b);
                     }
                 }
@@ -317,7 +326,7 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
         if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int e = warp - 4, quarter = warp & 3, half = e >> 2;
         const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::CW;
-        int it = 0;
+        int it = 0, round = 0;  // steps with column scales; handshakes
         for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
             const int m0 = (t % p.mt) * kM + quarter * 32, n0 = (t / p.mt) * NT + half * C::CW;
             float2 acc[C::CW / 2];
@@ -349,89 +358,105 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
             for (int r = 0; r < kRows; ++r) psa[r] = p.sa + min(m0 + (WIDE ? lane : (lane >> 2) + 8 * r), p.M - 1);
             const float* psb = p.sb + min(n0 / kBlock, p.NB - 1);
             float sa[kAhead][kRows], sb[kAhead];
+            auto fetch = [&](int slot, int kb) {
+                const bool there = kb < p.KB;
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
+                for (int r = 0; r < kRows; ++r) sa[slot][r] = there ? __ldg(psa[r] + (long long)kb * p.M) : 0.f;
+                sb[slot] = WIDE && there ? __ldg(psb + (long long)kb * p.NB) : 1.f;
+            };
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) sa[i][r] = i < p.KB ? __ldg(psa[r] + (long long)i * p.M) : 0.f;
-                sb[i] = WIDE && i < p.KB ? __ldg(psb + (long long)i * p.NB) : 1.f;
-            }
+            for (int i = 0; i < kAhead; ++i) fetch(i, i);
             bool ok = true;
-            for (int kb = 0; kb < p.KB; ++kb, ++it) {
-                const int b = it % C::kAcc, s = it % kScaleSlots;
-                const float* now = scales + s * NT + half * C::CW;
-                float s1[kRows];
+            for (int k0 = 0; k0 < p.KB; k0 += kStep, ++round) {
+                const int b = round % C::kAcc, steps = kStep == 1 ? 1 : min(kStep, p.KB - k0);
+                float s1[kStep][kRows];
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) s1[r] = sa[0][r] * sb[0];
+                for (int j = 0; j < kStep; ++j)
 #pragma unroll
-                for (int i = 0; i + 1 < kAhead; ++i) {
+                    for (int r = 0; r < kRows; ++r) s1[j][r] = sa[j][r] * sb[j];
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r) sa[i][r] = sa[i + 1][r];
-                    sb[i] = sb[i + 1];
+                for (int i = 0; i + kStep < kAhead; ++i) {
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) sa[i][r] = sa[i + kStep][r];
+                    sb[i] = sb[i + kStep];
                 }
-                if (kb + kAhead < p.KB) {
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r) sa[kAhead - 1][r] = __ldg(psa[r] + (long long)(kb + kAhead) * p.M);
-                    if (WIDE) sb[kAhead - 1] = __ldg(psb + (long long)(kb + kAhead) * p.NB);
-                }
-                ok = ok && ptx::mbar_wait(done + b, (it / C::kAcc) & 1);
+                for (int j = 0; j < kStep; ++j) fetch(kAhead - kStep + j, k0 + kAhead + j);
+                ok = ok && ptx::mbar_wait(done + b, (round / C::kAcc) & 1);
                 ptx::tc_fence_after();
                 // the next columns are on their way while a piece is added up
                 constexpr int kLd = C::CW >= 32 ? 32 : 16, kPieces = C::CW / kLd;
-                const uint32_t buf = mine + b * NT;
+                const uint32_t buf = mine + b * kStep * NT;
                 auto hand_back = [&]() {  // the buffer is read: the tensor core may fill it again
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(freed + b);
                 };
-                if constexpr (WIDE) {
-                    const float2 s2 = make_float2(s1[0], s1[0]);
-                    uint32_t v[2][kLd / 16][16];
-                    tmem_ld<kLd>(buf, v[0]);
+                // FULL: all kStep steps, which the compiler can then lay out in one go
+                auto add_up = [&](auto full) {
+                    constexpr bool FULL = decltype(full)::value;
+                    const int count = FULL ? kStep : steps;
+                    if constexpr (WIDE) {
+                        uint32_t v[2][kLd / 16][16];
+                        tmem_ld<kLd>(buf, v[0]);
 #pragma unroll
-                    for (int c = 0; c < kPieces; ++c) {
-                        tmem_wait<kLd>(v[c & 1]);
-                        if (c + 1 < kPieces) tmem_ld<kLd>(buf + (c + 1) * kLd, v[(c + 1) & 1]);
-                        else hand_back();
+                        for (int c = 0; c < kStep * kPieces; ++c) {
+                            const int j = c / kPieces, next = c + 1;
+                            if (FULL || j < count) {
+                                tmem_wait<kLd>(v[c & 1]);
+                                if (next < count * kPieces) tmem_ld<kLd>(buf + next / kPieces * NT + next % kPieces * kLd, v[next & 1]);
+                                else hand_back();
+                                const float2 s2 = make_float2(s1[j][0], s1[j][0]);
 #pragma unroll
-                        for (int i = 0; i < kLd / 2; ++i) {
-                            const uint32_t* w = &v[c & 1][i / 8][2 * (i % 8)];
-                            float2& to = acc[c * kLd / 2 + i];
-                            to = __ffma2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), s2, to);
+                                for (int i = 0; i < kLd / 2; ++i) {
+                                    const uint32_t* w = &v[c & 1][i / 8][2 * (i % 8)];
+                                    float2& to = acc[c % kPieces * kLd / 2 + i];
+                                    to = __ffma2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), s2, to);
+                                }
+                            }
                         }
-                    }
-                } else {
-                    // Column scales: a lane of the fragments needs a quarter of them, where a lane that holds a
-                    // whole row would read all from shared memory, 512 bytes a load and four columns (74 us
-                    // against 66 at 2048 x 2048 x 6400 in tiles of 128 columns).
-                    uint32_t v[2][2][kLd / 2];
-                    auto load = [&](int c) {
-                        tmem_ld_frag(buf + c * kLd, v[c & 1][0]);
-                        tmem_ld_frag(buf + c * kLd + (16u << 16), v[c & 1][1]);
-                    };
-                    const float* cs = now + 2 * (lane & 3);
-                    load(0);
+                    } else {
+                        // Column scales: a lane of the fragments needs a quarter of them, where a lane that holds a
+                        // whole row would read all from shared memory, 512 bytes a load and four columns (74 us
+                        // against 66 at 2048 x 2048 x 6400 in tiles of 128 columns).
+                        uint32_t v[2][2][kLd / 2];
+                        auto load = [&](int c) {
+                            const uint32_t from = buf + c / kPieces * NT + c % kPieces * kLd;
+                            tmem_ld_frag(from, v[c & 1][0]);
+                            tmem_ld_frag(from + (16u << 16), v[c & 1][1]);
+                        };
+                        load(0);
 #pragma unroll
-                    for (int c = 0; c < kPieces; ++c) {
-                        tmem_wait(v[c & 1][0]);
-                        tmem_wait(v[c & 1][1]);
-                        if (c + 1 < kPieces) load(c + 1);
-                        else hand_back();
+                        for (int c = 0; c < kStep * kPieces; ++c) {
+                            const int j = c / kPieces, next = c + 1;
+                            if (FULL || j < count) {
+                                const float* cs = scales + (it + j) % kScaleSlots * NT + half * C::CW + 2 * (lane & 3);
+                                tmem_wait(v[c & 1][0]);
+                                tmem_wait(v[c & 1][1]);
+                                if (next < count * kPieces) load(next);
+                                else hand_back();
 #pragma unroll
-                        for (int i = 0; i < kLd / 8; ++i) {
-                            const float2 k2 = *reinterpret_cast<const float2*>(cs + c * kLd + 8 * i);
+                                for (int i = 0; i < kLd / 8; ++i) {
+                                    const float2 k2 = *reinterpret_cast<const float2*>(cs + c % kPieces * kLd + 8 * i);
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const uint32_t* w = &v[c & 1][r / 2][4 * i + 2 * (r % 2)];
-                                const float2 f = __fmul2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), k2);
-                                float2& to = acc[(c * kLd / 8 + i) * 4 + r];
-                                to = __ffma2_rn(f, make_float2(s1[r], s1[r]), to);
+                                    for (int r = 0; r < 4; ++r) {
+                                        const uint32_t* w = &v[c & 1][r / 2][4 * i + 2 * (r % 2)];
+                                        const float2 f = __fmul2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), k2);
+                                        float2& to = acc[(c % kPieces * kLd / 8 + i) * 4 + r];
+                                        to = __ffma2_rn(f, make_float2(s1[j][r], s1[j][r]), to);
+                                    }
+                                }
                             }
                         }
                     }
-                }
+                };
+                if (kStep == 1 || steps == kStep) add_up(std::true_type{});
+                else add_up(std::false_type{});
                 if (!WIDE) {
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(sempty + s);
+                    if (lane == 0)
+                        for (int j = 0; j < steps; ++j) ptx::mbar_arrive(sempty + (it + j) % kScaleSlots);
+                    it += steps;
                 }
             }
             if (!ok) {  // never expected: a wait ran out of time; NaN rather than a partial sum
