@@ -157,7 +157,7 @@ def load():
     L.mh3a_fp8_quantize.restype = i
     L.mh3a_fp8_matmul.argtypes = [vp, ll, vp, vp, ll, vp, i, i, i, i, vp, i, vp, ll, vp]
     L.mh3a_fp8_matmul.restype = i
-    L.mh3a_fp8_linear_workspace.argtypes = [i, i]
+    L.mh3a_fp8_linear_workspace.argtypes = [i, i, i]
     L.mh3a_fp8_linear_workspace.restype = sz
     L.mh3a_fp8_linear.argtypes = [vp, i, ll, vp, ll, vp, i, i, i, i, vp, vp, ll, vp, sz, vp]
     L.mh3a_fp8_linear.restype = i

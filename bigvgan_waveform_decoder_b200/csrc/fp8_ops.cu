@@ -1,9 +1,9 @@
 // fp8_ops.cu -- entry points of the fp8 operators, and the linear layer of a few rows.
 //
 // Few rows (a decode frame by frame): the product is bound by reading the weights once, 1 byte each,
-// so it runs on the CUDA cores: a warp takes two weight rows, a lane 16 bytes of each at a time; the
-// rows of x are quantised by every block for itself (2 KB to 64 KB of input from L2) instead of by a
-// launch of its own.
+// so it runs on the CUDA cores: a warp takes two weight rows, a lane 16 bytes of each at a time, the next
+// 2048 columns on their way while the present ones are multiplied; the
+// rows of x are quantised by every block for itself (from L2) instead of by a launch of its own.
 #include "fp8_kernels.cuh"
 
 namespace mh3a {
@@ -47,9 +47,8 @@ __global__ void __launch_bounds__(kThreads) k_fp8_few_rows(const FewRowsArgs a, 
 #pragma unroll
         for (int m = 0; m < MR; ++m) acc[r][m] = 0.f;
     const int NB = (a.N + a.w_block_rows - 1) / a.w_block_rows;
-    for (int k0 = 0; k0 < a.K; k0 += kSlab) {
-        // the weights of the slab are on their way while x is quantised
-        uint4 w[RW][kSteps];
+    // a lane's 16 bytes of each row and step, from slab k0
+    auto fetch = [&](uint4(&w)[RW][kSteps], int k0) {
 #pragma unroll
         for (int r = 0; r < RW; ++r)
 #pragma unroll
@@ -59,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) k_fp8_few_rows(const FewRowsArgs a, 
                 if (n < a.N && k < a.K) {
                     const unsigned char* from = a.w + (long long)n * a.ws + k;
                     if (k + kLane <= a.K) {
-                        w[r][t] = __ldg(reinterpret_cast<const uint4*>(from));
+                        w[r][t] = __ldcs(reinterpret_cast<const uint4*>(from));
                     } else {
                         uint32_t q[4] = {0, 0, 0, 0};
                         for (int i = 0; i < a.K - k; ++i) q[i >> 2] |= (uint32_t)from[i] << (8 * (i & 3));
@@ -67,6 +66,15 @@ __global__ void __launch_bounds__(kThreads) k_fp8_few_rows(const FewRowsArgs a, 
                     }
                 }
             }
+    };
+    uint4 next[RW][kSteps];
+    fetch(next, 0);
+    for (int k0 = 0; k0 < a.K; k0 += kSlab) {
+        uint4 w[RW][kSteps];
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+#pragma unroll
+            for (int t = 0; t < kSteps; ++t) w[r][t] = next[r][t];
         if (k0) __syncthreads();
         // 16 values a lane, 8 lanes a block of 128
         for (int j = warp; j < MR * kSteps; j += kWarps) {
@@ -92,6 +100,7 @@ __global__ void __launch_bounds__(kThreads) k_fp8_few_rows(const FewRowsArgs a, 
                 xs[m][t][i][lane] = make_float4(u[4 * i] * s, u[4 * i + 1] * s, u[4 * i + 2] * s, u[4 * i + 3] * s);
         }
         __syncthreads();
+        if (k0 + kSlab < a.K) fetch(next, k0 + kSlab);  // on their way while this slab is added up
 #pragma unroll
         for (int t = 0; t < kSteps; ++t) {
             const int k = k0 + (t * 32 + lane) * kLane;
@@ -147,9 +156,7 @@ int few(const FewRowsArgs& a, cudaStream_t s) {
 
 template <typename T>
 int few(const FewRowsArgs& a, cudaStream_t s) {
-    if (a.M == 1) return few<T, 1>(a, s);
-    if (a.M == 2) return few<T, 2>(a, s);
-    return few<T, 4>(a, s);
+    return a.M == 1 ? few<T, 1>(a, s) : a.M == 2 ? few<T, 2>(a, s) : few<T, 4>(a, s);
 }
 
 constexpr int kMostSize = 1 << 30;
@@ -161,6 +168,12 @@ bool stored_ok(const void* q, long long stride, int cols) {
     return q && aligned(q, 16) && stride >= cols && stride % 16 == 0 && stride < (1LL << 40);
 }
 long long blocks(int n) { return (n + (long long)kBlock - 1) / kBlock; }
+
+// Whether a layer takes the kernel for few rows; its multiplications are the CUDA cores', so the tensor
+// cores overtake it where there are many.  Measured, us, this kernel against quantisation and product:
+// 1 row 2048 x 2048 3.4 / 6.9, 2048 x 8192 7.0 / 8.1, 8192 x 8192 25.7 / 20.7; 2 rows 4096 x 4096 7.7 / 11.0;
+// 4 rows 2048 x 2048 5.2 / 6.9, 4096 x 4096 12.0 / 11.1, 8192 x 8192 42.2 / 21.1.
+bool few_rows(int M, int N, int K) { return M <= MH3A_FP8_FEW_ROWS && (long long)M * N * K <= 48LL << 20; }
 
 // Layout of mh3a_fp8_linear's scratch: x quantised, then its scales.
 long long q_stride(int K) { return (K + 15LL) / 16 * 16; }
@@ -220,8 +233,8 @@ extern "C" MH3A_API mh3a_status mh3a_fp8_matmul(const void* a, long long a_strid
     return launch_matmul(m, static_cast<cudaStream_t>(stream)) < 0 ? launch_failed("mh3a_fp8_matmul") : MH3A_OK;
 }
 
-extern "C" MH3A_API size_t mh3a_fp8_linear_workspace(int M, int K) {
-    if (!size_ok(M) || !size_ok(K) || M <= MH3A_FP8_FEW_ROWS) return 0;
+extern "C" MH3A_API size_t mh3a_fp8_linear_workspace(int M, int N, int K) {
+    if (!size_ok(M) || !size_ok(N) || !size_ok(K) || few_rows(M, N, K)) return 0;
     return q_bytes(M, K) + (size_t)blocks(K) * M * 4;
 }
 
@@ -233,17 +246,11 @@ extern "C" MH3A_API mh3a_status mh3a_fp8_linear(const void* x, int dtype, long l
     if (st != MH3A_OK) return st;
     if (x_stride < 0 || !aligned(x, elem(dtype))) return MH3A_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (M <= MH3A_FP8_FEW_ROWS) {
-        // four rows at a time, so that the weights' second reading comes from L2
-        for (int m = 0; m < M; m += 4) {
-            const FewRowsArgs f{static_cast<const char*>(x) + (long long)m * x_stride * elem(dtype), x_stride,
-                                static_cast<const unsigned char*>(w), w_stride, w_scale, w_block_rows, M - m < 4 ? M - m : 4, N, K, bias,
-                                static_cast<char*>(y) + (long long)m * y_stride * elem(dtype), y_stride};
-            if (launch_few_rows(f, dtype, s) < 0) return launch_failed("mh3a_fp8_linear");
-        }
-        return MH3A_OK;
+    if (few_rows(M, N, K)) {
+        const FewRowsArgs f{x, x_stride, static_cast<const unsigned char*>(w), w_stride, w_scale, w_block_rows, M, N, K, bias, y, y_stride};
+        return launch_few_rows(f, dtype, s) < 0 ? launch_failed("mh3a_fp8_linear") : MH3A_OK;
     }
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < mh3a_fp8_linear_workspace(M, K)) return MH3A_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < mh3a_fp8_linear_workspace(M, N, K)) return MH3A_ERR_INVALID_ARG;
     unsigned char* q = static_cast<unsigned char*>(workspace);
     float* scale = reinterpret_cast<float*>(q + q_bytes(M, K));
     const mh3a_status sq = mh3a_fp8_quantize(x, dtype, M, K, x_stride, 1, 0, q, q_stride(K), scale, stream);

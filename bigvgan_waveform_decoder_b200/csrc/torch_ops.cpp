@@ -312,7 +312,7 @@ Tensor fp8_linear(const Tensor& x, const Tensor& w, const Tensor& w_scale, const
     check_bias_out(what, bias, out, x.device(), M, N, x.scalar_type());
     const Launch on(x.device(), stream);
     const Tensor y = out ? *out : empty({M, N}, x.scalar_type(), x.device());
-    const size_t n = mh3a_fp8_linear_workspace((int)M, (int)K);
+    const size_t n = mh3a_fp8_linear_workspace((int)M, (int)N, (int)K);
     Tensor ws;
     if (n) ws = empty({(int64_t)n}, at::kByte, x.device());
     check(mh3a_fp8_linear(x.data_ptr(), dtype_of(x.scalar_type()), row_stride(x, K), w.data_ptr(), sw.stride,

@@ -410,12 +410,13 @@ MH3A_API mh3a_status mh3a_fp8_matmul(const void* a, long long a_stride, const fl
 
 /* y = x w^T + bias for activations x [M, K] of `dtype` (columns adjacent, rows x_stride >= 0 elements
  * apart) and quantised weights w [N, K]: mh3a_fp8_quantize of x with block_rows 1, then
- * mh3a_fp8_matmul with y of the same dtype.  Up to MH3A_FP8_FEW_ROWS rows it is one kernel that is
- * bound by reading the weights, for a decode frame by frame.  `workspace`: device, 16-byte aligned,
- * mh3a_fp8_linear_workspace bytes (0 for few rows; it may be NULL then).  Errors: as the two calls,
- * and MH3A_ERR_INVALID_ARG for a workspace too small or misaligned. */
-#define MH3A_FP8_FEW_ROWS 8
-MH3A_API size_t mh3a_fp8_linear_workspace(int M, int K);
+ * mh3a_fp8_matmul with y of the same dtype.  One to MH3A_FP8_FEW_ROWS rows of a layer that is not
+ * large run as one kernel that is bound by reading the weights, for a decode frame by frame.
+ * `workspace`: device, 16-byte aligned, mh3a_fp8_linear_workspace(M, N, K) bytes (0 for that kernel;
+ * it may be NULL then).  Errors: as the two calls, and MH3A_ERR_INVALID_ARG for a workspace too small
+ * or misaligned. */
+#define MH3A_FP8_FEW_ROWS 4
+MH3A_API size_t mh3a_fp8_linear_workspace(int M, int N, int K);
 MH3A_API mh3a_status mh3a_fp8_linear(const void* x, int dtype, long long x_stride, const void* w, long long w_stride,
                                      const float* w_scale, int w_block_rows, int M, int N, int K, const float* bias,
                                      void* y, long long y_stride, void* workspace, size_t workspace_bytes,

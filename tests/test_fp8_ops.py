@@ -181,7 +181,7 @@ def test_matmul_padded_operands_and_strided_output(dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("shape", [(1, 1, 1), (1, 2048, 2048), (1, 8, 32), (2, 100, 130), (3, 1000, 2049), (4, 17, 5000), (5, 64, 256),
-                                   (8, 2048, 1336), (9, 300, 500), (64, 2048, 2048), (517, 1000, 1336)], ids=str)
+                                   (8, 2048, 1336), (9, 300, 500), (64, 2048, 2048), (1, 4100, 12300), (3, 8200, 4096), (517, 1000, 1336)], ids=str)
 @pytest.mark.parametrize("w_rows", (1, 128))
 def test_linear(shape, w_rows, dtype):
     M, N, K = shape
@@ -365,15 +365,16 @@ def test_abi_refusals():
         assert mm(**kw) == 3, kw
 
     def lin(x=ok, dt=2, xs=256, w=ok, ws=256, sw=ok, br=128, M=10, N=300, K=256, bias=None, y=ok, ys=300, wk=ok,
-            n=L.mh3a_fp8_linear_workspace(10, 256)):
+            n=L.mh3a_fp8_linear_workspace(10, 300, 256)):
         return L.mh3a_fp8_linear(x, dt, xs, w, ws, sw, br, M, N, K, bias, y, ys, wk, n, None)
 
     for kw in (dict(x=None), dict(w=None), dict(sw=None), dict(y=None), dict(wk=None), dict(wk=ok + 8), dict(n=10), dict(xs=-1),
                dict(x=ok + 1), dict(dt=7), dict(ws=128), dict(ys=10), dict(br=3)):
         assert lin(**kw) == 1, kw
     assert lin(M=0) == 3 and lin(K=0) == 3
-    assert L.mh3a_fp8_linear_workspace(8, 256) == 0 and L.mh3a_fp8_linear_workspace(9, 256) >= 9 * (256 + 8)
-    assert L.mh3a_fp8_linear_workspace(0, 256) == 0 and L.mh3a_fp8_linear_workspace(9, -1) == 0
+    size = L.mh3a_fp8_linear_workspace
+    assert size(4, 300, 256) == 0 and size(5, 300, 256) >= 5 * (256 + 8) and size(1, 8192, 8192) >= 8192 + 64 * 4
+    assert size(0, 300, 256) == 0 and size(9, 300, -1) == 0 and size(9, 0, 256) == 0
 
 
 def test_exports():
