@@ -228,7 +228,8 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
     uint64_t* freed = done + C::kAcc;     // and read again
     uint64_t* sfull = freed + C::kAcc;    // scales of a step are there
     uint64_t* sempty = sfull + kScaleSlots;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + kScaleSlots);
+    uint64_t* drain = sempty + kScaleSlots;  // only after a wait that ran out of time
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0 && lane == 0) {
@@ -240,6 +241,7 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
             ptx::mbar_init(done + i, WIDE ? 1 : 2);  // the MMAs; and the step's column scales
             ptx::mbar_init(freed + i, C::EW);
         }
+        ptx::mbar_init(drain, 1);
         for (int i = 0; i < kScaleSlots; ++i) {
             ptx::mbar_init(sfull + i, 32);
             ptx::mbar_init(sempty + i, C::EW);
@@ -304,6 +306,10 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                         if (lane == 0) ptx::mbar_arrive(done + b);
                     }
                 }
+            }
+            if (!ok) {  // the MMAs on their way end before tensor memory is given back
+                ptx::mma_commit_elect(drain);
+                ptx::mbar_wait(drain, 0);
             }
         } else if (warp == 2 && !WIDE) {
             int it = 0;
