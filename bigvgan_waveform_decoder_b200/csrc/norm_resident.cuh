@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
 #pragma unroll
         for (int off = 8; off; off >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, off);
         if (lane == 0) {
-            const float rstd = 1.0f / sqrtf((float)(m2 * inv_count + (double)a.eps));
+            // equal values leave a sum of squares within rounding of 0, on either side (NaN stays)
+            const float rstd = 1.0f / sqrtf((float)((m2 < 0.0 ? 0.0 : m2 * inv_count) + (double)a.eps));
             fin[g] = make_float2((float)mean, rstd);
             if (p.rank == 0) {
                 const long long at = (long long)p.b * a.G + p.c0 / a.D + g;

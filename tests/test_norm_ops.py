@@ -369,3 +369,18 @@ def test_tensors_that_are_not_on_a_gpu_are_refused():
 
 def test_exports():
     assert {"mh3a_group_norm_act", "mh3a_group_norm_act_backward", "mh3a_group_norm_act_workspace"} <= set(Bd.EXPORTS)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("shape", [(64, 4, 64, 4), (64, 161, 200, 8), (64, 1034, 200, 8), (64, 50, 25, 5), (2, 60000, 96, 3)], ids=str)
+def test_equal_values_far_from_zero(shape, dtype):
+    """Every value of an item alike and large: the variance is 0, and rounding must not take it below."""
+    B, T, Cn, G = shape
+    g = torch.Generator().manual_seed(T)
+    x = (10 ** (4 + 6 * torch.rand(B, 1, 1, generator=g)) * torch.randn(B, 1, 1, generator=g).sign()).to(TYPES[dtype])
+    x = x.repeat(1, T, Cn).cuda()
+    y, mean, rstd = pkg.group_norm_act(x, G, eps=1e-12)
+    assert torch.equal(mean, x[:, 0, :1].float().expand(B, G)) and torch.all(y == 0)
+    # nothing but eps under the root, or what the squares of half units of the values leave
+    assert torch.all(rstd > 0) and torch.all(rstd <= 1e6 * (1 + 4 * R.F24))
