@@ -673,15 +673,16 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 template <typename Extra>
 bool plan_resident(const NormArgs& a, int V, int e, int bytes_row, Extra extra, Resident* r) {
     const long long unit_l = (long long)a.D / gcd(a.D, V) * V;
-    if (unit_l > kResThreads * V || a.B > 65535 || (long long)a.B * a.T * a.C * bytes_row > kResMax) return false;
-    const int unit = (int)unit_l, units = a.C / unit;
+    if (unit_l > kResThreads * V || a.B > 65535 || (long long)a.B * a.C * a.T > kResMax / bytes_row) return false;
+    const int unit = (int)unit_l, units = a.C / unit, most = kResThreads * V / unit;
     for (int limit : {kResTwo, kResOne}) {
         for (int want : {128, 64}) {
             int k = 1;
-            while (k < units && (units % k || k * unit * e < want)) ++k;
+            while (k < units && k <= most && (units % k || k * unit * e < want)) ++k;
+            if (k > most) continue;  // wider than a row of threads
             const int W = k * unit;
             const int slabs = a.C / W;
-            if (slabs > 65535 || W / V > kResThreads) continue;
+            if (slabs > 65535) continue;
             // narrower slabs while whole clusters of wide ones would leave SMs idle
             if (want == 128 && k > 1 && (long long)a.B * slabs * 8 < 2 * kSms && a.T >= 128) continue;
             auto bytes = [&](int s) { return (long long)((a.T + s - 1) / s) * W * bytes_row + extra(W, s); };

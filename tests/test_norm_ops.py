@@ -1,5 +1,6 @@
 """Group norm with an activation over channels-last frames, against its formulas in 64 bits."""
 import ctypes as C
+import time
 
 import pytest
 import torch
@@ -384,3 +385,13 @@ def test_equal_values_far_from_zero(shape, dtype):
     assert torch.equal(mean, x[:, 0, :1].float().expand(B, G)) and torch.all(y == 0)
     # nothing but eps under the root, or what the squares of half units of the values leave
     assert torch.all(rstd > 0) and torch.all(rstd <= 1e6 * (1 + 4 * R.F24))
+
+
+def test_planning_takes_no_time_for_any_width():
+    """Channels whose count has no small divisor: the search for a slab is bounded."""
+    L = Bd.load()
+    p = norm(dtype=0, B=1, T=1, C=4 * 5999993, groups=4 * 5999993)
+    t0 = time.perf_counter()
+    for _ in range(20):
+        assert L.mh3a_group_norm_act_workspace(C.byref(p), 0, 1) > 0
+    assert time.perf_counter() - t0 < 0.2
