@@ -942,6 +942,9 @@ extern "C" MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p,
     if (p->act != MH3A_ACT_SNAKE_BETA && (dalpha || dbeta)) return MH3A_ERR_INVALID_ARG;
     const int e = elem_bytes(p->dtype);
     if (!aligned(x, e) || !aligned(dy, e) || !aligned(dx, e)) return MH3A_ERR_INVALID_ARG;
+    for (const float* f : {mean, rstd, static_cast<const float*>(dweight), static_cast<const float*>(dbias),
+                           static_cast<const float*>(dalpha), static_cast<const float*>(dbeta)})
+        if (!aligned(f, 4)) return MH3A_ERR_INVALID_ARG;
     NormArgs a = base_args(p);
     a.x = x;
     a.xb = x_batch_stride;

@@ -395,3 +395,12 @@ def test_planning_takes_no_time_for_any_width():
     for _ in range(20):
         assert L.mh3a_group_norm_act_workspace(C.byref(p), 0, 1) > 0
     assert time.perf_counter() - t0 < 0.2
+
+
+def test_abi_refuses_misaligned_statistics_and_gradients():
+    L, ok = Bd.load(), 1 << 20
+    p = norm(act=2, alpha=ok, beta=ok)
+    n = L.mh3a_group_norm_act_workspace(C.byref(p), 1, 0)
+    for bad in range(6):
+        f = [ok + 2 * (i == bad) for i in range(6)]
+        assert L.mh3a_group_norm_act_backward(C.byref(p), ok, 240, 24, ok, 240, 24, f[0], f[1], ok, *f[2:], ok, n, None) == 1
