@@ -413,7 +413,7 @@ MH3A_API mh3a_status mh3a_fp8_matmul(const void* a, long long a_stride, const fl
  * mh3a_fp8_matmul with y of the same dtype.  One to MH3A_FP8_FEW_ROWS rows of a layer that is not
  * large run as one kernel that is bound by reading the weights, for a decode frame by frame.
  * `workspace`: device, 16-byte aligned, mh3a_fp8_linear_workspace(M, N, K) bytes (0 for that kernel;
- * it may be NULL then).  Errors: as the two calls, and MH3A_ERR_INVALID_ARG for a workspace too small
+ * it may be NULL then).  y must not overlap x or w.  Errors: as the two calls, and MH3A_ERR_INVALID_ARG for a workspace too small
  * or misaligned. */
 #define MH3A_FP8_FEW_ROWS 4
 MH3A_API size_t mh3a_fp8_linear_workspace(int M, int N, int K);

@@ -380,3 +380,20 @@ def test_abi_refusals():
 def test_exports():
     assert {"mh3a_fp8_quantize", "mh3a_fp8_matmul", "mh3a_fp8_linear", "mh3a_fp8_linear_workspace"} <= set(Bd.EXPORTS)
     assert C.sizeof(Bd.mh3a_norm) == 72
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", (2, 300))
+def test_an_output_over_an_operand_is_refused(M):
+    x = rand(M, 256)
+    w, sw = pkg.fp8_quantize(rand(256, 256), block_rows=128)
+    q, s = pkg.fp8_quantize(x)
+    over = q.view(torch.float32).as_strided((M, 64), (64, 1))
+    wn, swn = w[:64], sw[:, :1].contiguous()
+    for bad in (lambda: pkg.fp8_linear(x, w, sw, out=x), lambda: pkg.fp8_matmul(q, s, wn, swn, torch.float32, out=over)):
+        with pytest.raises(pkg.MH3AError, match="overlaps") as e:
+            bad()
+        assert e.value.status == 1
+    # columns of one buffer side by side
+    buf = torch.cat((x, torch.zeros_like(x)), 1)
+    assert torch.equal(pkg.fp8_linear(buf[:, :256], w, sw, out=buf[:, 256:]), pkg.fp8_linear(x, w, sw))

@@ -404,3 +404,19 @@ def test_abi_refuses_misaligned_statistics_and_gradients():
     for bad in range(6):
         f = [ok + 2 * (i == bad) for i in range(6)]
         assert L.mh3a_group_norm_act_backward(C.byref(p), ok, 240, 24, ok, 240, 24, f[0], f[1], ok, *f[2:], ok, n, None) == 1
+
+
+@pytest.mark.gpu
+def test_an_output_over_its_input_is_refused():
+    x = torch.randn(3, 5, 64, device="cuda")
+    buf = torch.zeros(2 * x.numel() + 32, device="cuda")
+    part = buf[16:16 + x.numel()].view(x.shape)
+    for bad in (lambda: pkg.group_norm_act(x, 4, out=x), lambda: pkg.group_norm_act(part, 4, out=buf[:x.numel()].view(x.shape))):
+        with pytest.raises(pkg.MH3AError, match="overlaps") as e:
+            bad()
+        assert e.value.status == 1
+    out = buf[x.numel() + 16:]
+    with pytest.raises(pkg.MH3AError):
+        pkg.group_norm_act(x, 4, out=out)
+    y, *_ = pkg.group_norm_act(part, 4, out=buf[-x.numel():].view(x.shape))  # side by side in one storage
+    assert torch.all(y == 0)
