@@ -397,3 +397,39 @@ def test_an_output_over_an_operand_is_refused(M):
     # columns of one buffer side by side
     buf = torch.cat((x, torch.zeros_like(x)), 1)
     assert torch.equal(pkg.fp8_linear(buf[:, :256], w, sw, out=buf[:, 256:]), pkg.fp8_linear(x, w, sw))
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    """Matrices of more than 2^31 elements, and rows far apart: the last rows are where they belong."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = (1 << 21) + 5
+    x = torch.empty(rows, 1024, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    for block_rows in (1, 128):
+        q, s = pkg.fp8_quantize(x, block_rows=block_rows)
+        last = x[rows - 133:]  # from a block's first row
+        rq, rs, _ = R.quantize(last, block_rows)
+        assert torch.equal(q[rows - 133:].float().double(), rq)
+        assert torch.equal((s[:, rows - 133:] if block_rows == 1 else s[:, -2:]).double(), rs)
+        q, s = pkg.fp8_quantize(x, block_rows=block_rows, transpose=True)
+        rq, rs, _ = R.quantize(last.t(), block_rows)
+        assert torch.equal(q[:, rows - 133:].float().double(), rq) and torch.equal(s[-2:].double(), rs)
+    del q, s, rq
+    M, N, K = (1 << 20) + 3, 2056, 136
+    a, sa = pkg.fp8_quantize(x.view(-1)[:M * K].view(M, K))
+    b, sb = pkg.fp8_quantize(x[:N, :K], block_rows=128)
+    out = pkg.fp8_matmul(a, sa, b, sb)
+    for k in (0, M - 131):
+        check_product(out[k:][:131], a[k:][:131], sa[:, k:][:, :131].contiguous(), b, sb)
+    del out
+    # 3 rows 2^30 and more elements apart: one layer of few rows, one of more
+    wide = x.view(-1).as_strided((3, 1024), ((1 << 30) + 16, 1))
+    w, sw = pkg.fp8_quantize(x[:200, :1024], block_rows=1)
+    assert torch.equal(pkg.fp8_linear(wide, w, sw), pkg.fp8_linear(wide.contiguous(), w, sw))
+    store = torch.empty(3 * (1 << 30), device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+    far = store.as_strided((3, 1024), ((1 << 30) + 16, 1))
+    far.copy_(w[:3])
+    sf = sw[:, :3].contiguous()
+    assert torch.equal(pkg.fp8_matmul(w, sw, far, sf), pkg.fp8_matmul(w, sw, w[:3], sf))
+    assert torch.equal(pkg.fp8_matmul(far, sf, w, sw), pkg.fp8_matmul(w[:3], sf, w, sw))
+    assert torch.equal(pkg.fp8_linear(x[:2], far, sf), pkg.fp8_linear(x[:2], w[:3], sf))

@@ -420,3 +420,34 @@ def test_an_output_over_its_input_is_refused():
         pkg.group_norm_act(x, 4, out=out)
     y, *_ = pkg.group_norm_act(part, 4, out=buf[-x.numel():].view(x.shape))  # side by side in one storage
     assert torch.all(y == 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", (9, 40000))
+def test_parameters_off_16_bytes(T, dtype):
+    x, *params = case(2, T, 64, "snake_beta", dtype, seed=T)
+    params = [torch.cat((p[:1], p))[1:] for p in params]
+    assert all(p.data_ptr() % 16 for p in params)
+    w, b, al, be = params
+    _, mean, rstd = check_forward(x, 4, w, b, "snake_beta", al, be)
+    check_backward(torch.flip(x, (1,)), x, mean, rstd, 4, w, b, "snake_beta", al, be)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", (8, 1024))
+def test_offsets_beyond_32_bits(T):
+    """Items whose elements lie more than 2^31 from the tensor's start: 2^31 elements in a row, and far strides."""
+    Cn, G, B = 1024, 32, 2100
+    g = torch.Generator(device="cuda").manual_seed(1)
+    if T == 1024:
+        x = torch.empty(B, T, Cn, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    else:
+        x = torch.empty((1 << 31) + 3 * T * Cn, device="cuda", dtype=torch.bfloat16).as_strided((3, T, Cn), ((1 << 30) + 8 * Cn, Cn, 1))
+        x.normal_(generator=g)
+    y, mean, rstd = pkg.group_norm_act(x, G, act="silu")
+    dx, *_ = pkg.group_norm_act_backward(x, x, mean, rstd, G, act="silu")
+    for i in (0, -1):
+        one, m, r = x[i:][:1], mean[i:][:1], rstd[i:][:1]
+        check_forward(one, G, None, None, "silu", None, None, got=(y[i:][:1], m, r))
+        check_backward(one, one, m, r, G, None, None, "silu", None, None, got=(dx[i:][:1], None, None, None, None))
