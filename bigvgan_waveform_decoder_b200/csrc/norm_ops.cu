@@ -625,7 +625,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_norm_bwd_apply(const NormArgs a
 }
 
 // ------------------------------------------------------------------------------------- host
-constexpr int kFwdPerSm = 4, kBwdPerSm = 8;
+// Blocks for each SM, and the most rows of a thread.
+struct Split {
+    int per_sm, most_rows;
+};
+constexpr Split kFwdSplit{4, 80}, kBwdSplit{8, 128};
 
 int pow2_ceil(long long n, int most) {
     int p = 1;
@@ -634,17 +638,22 @@ int pow2_ceil(long long n, int most) {
 }
 
 // Threads, channel tiles and row chunks for vectors of V channels.  Chunks are as many as give every
-// SM `per_sm` blocks, but of at least 4 rows a thread.  Measured on sixteen 20 s items (256 channels,
-// bf16): forward 100 us with 4, 106 with 8, 110 with 12; backward with unequal lengths, where blocks
+// SM `per_sm` blocks, but of 4 to `most_rows` rows a thread.  The upper end bounds what rounding does to a
+// thread's fp32 sums: with outliers of 10^5 deviations among a thread's first rows, rstd is off by 18
+// units of 2^-24 at most with 80 rows, 43 with 128, 8000 with 1250 (100 fp32 items of [20000, 256]).  Short
+// chunks also even out the last round of blocks: there forward 1021 us with 80 rows, 1042 with 128, 1225 with
+// no bound; backward (plain sums) bf16 [1200, 8000, 256] 3829 with 64, 3662 with 128, 3740 with no bound.
+// Blocks for each SM, measured on sixteen 20 s items (256 channels, bf16): forward 100 us with 4, 106 with 8, 110 with 12; backward with unequal lengths, where blocks
 // behind an item's end have nothing to do, 117, 112 and 115.
-void plan_general(NormArgs* a, int V, int per_sm) {
+void plan_general(NormArgs* a, int V, Split split) {
     const long long cvecs = ((long long)a->C + V - 1) / V;
     a->tx = pow2_ceil(cvecs, 32);
     a->ctiles = (int)((cvecs + a->tx - 1) / a->tx);
     const int ty = kThreads / a->tx;
-    const long long want = std::max<long long>(1, (long long)per_sm * kSms / std::max<long long>(1, (long long)a->ctiles * a->B));
+    const long long want = std::max<long long>(1, (long long)split.per_sm * kSms / std::max<long long>(1, (long long)a->ctiles * a->B));
     const long long most = std::max<long long>(1, ((long long)a->T + 4 * ty - 1) / (4 * ty));
-    a->chunks = (int)std::min(want, most);
+    const long long least = ((long long)a->T + split.most_rows * ty - 1) / (split.most_rows * ty);
+    a->chunks = (int)std::max(std::min(want, most), least);
     a->rows = (a->T + a->chunks - 1) / a->chunks;
     a->chunks = (a->T + a->rows - 1) / a->rows;
 }
@@ -723,7 +732,7 @@ int general_width(int V, int backward) { return backward ? std::min(V, 4) : V; }
 
 // Scratch of the general form with vectors of V channels.
 size_t general_bytes(NormArgs a, int act, int backward, int V) {
-    plan_general(&a, V, backward ? kBwdPerSm : kFwdPerSm);
+    plan_general(&a, V, backward ? kBwdSplit : kFwdSplit);
     const long long ns = act == MH3A_ACT_SNAKE_BETA ? 4 : 2;
     long long floats = (long long)a.B * a.chunks * (backward ? a.C * ns : (a.G + a.ctiles) * 4LL);
     if (backward) floats += ((long long)a.B * a.C * ns + 3) / 4 * 4 + 2LL * a.B * a.G;
@@ -789,7 +798,7 @@ bool forward(NormArgs& a, const Way& w, int act, int width, cudaStream_t s) {
             default: return forward_resident<T, V, MH3A_ACT_NONE>(a, w.r, s);
         }
     }
-    plan_general(&a, general_width(width, 0), kFwdPerSm);
+    plan_general(&a, general_width(width, 0), kFwdSplit);
     if constexpr (V == 8) {
         if (width == 8) return forward_general<T, 8>(a, act, s);
     }
@@ -821,7 +830,7 @@ bool backward_act(NormArgs& a, const Way& w, int width, cudaStream_t s) {
         return go(k_norm_bwd_final, ((long long)a.C * NS + 31) / 32, 256, s, a, (const float*)a.ws, (float2*)nullptr, NS, 0);
     }
     width = general_width(width, 1);
-    plan_general(&a, width, kBwdPerSm);
+    plan_general(&a, width, kBwdSplit);
     if (width == 4) return backward_general<T, 4, ACT>(a, s);
     return width == 2 ? backward_general<T, 2, ACT>(a, s) : backward_general<T, 1, ACT>(a, s);
 }
@@ -843,9 +852,10 @@ mh3a_status check(const mh3a_norm* p) {
     if (p->act < MH3A_ACT_NONE || p->act > MH3A_ACT_SNAKE_BETA) return MH3A_ERR_INVALID_ARG;
     if (p->B < 1 || p->T < 1 || p->C < 1 || p->groups < 1 || p->C % p->groups) return MH3A_ERR_SHAPE;
     if (p->act == MH3A_ACT_SNAKE_BETA && (!p->alpha || !p->beta)) return MH3A_ERR_INVALID_ARG;
-    // row indices plus a block's stride stay in 32 bits; grids (at most one block per item and channel)
-    // stay below 2^31
-    if (p->T > (1 << 30) || (long long)p->B * p->C >= (1LL << 31)) return MH3A_ERR_SHAPE;
+    // row indices plus a block's stride stay in 32 bits; grids (at most one block per item and channel, or
+    // for 64 x 256 values) stay below 2^31
+    if (p->T > (1 << 30) || (long long)p->B * p->C >= (1LL << 31) || (long long)p->B * p->C * p->T >= (1LL << 40))
+        return MH3A_ERR_SHAPE;
     return MH3A_OK;
 }
 

@@ -451,3 +451,24 @@ def test_offsets_beyond_32_bits(T):
         one, m, r = x[i:][:1], mean[i:][:1], rstd[i:][:1]
         check_forward(one, G, None, None, "silu", None, None, got=(y[i:][:1], m, r))
         check_backward(one, one, m, r, G, None, None, "silu", None, None, got=(dx[i:][:1], None, None, None, None))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+def test_outliers_in_a_large_batch(dtype):
+    """So many items that one block could take all rows of one: a thread's sums must not grow long."""
+    x = torch.empty(300, 6000, 256, device="cuda", dtype=TYPES[dtype]).normal_(generator=torch.Generator(device="cuda").manual_seed(4))
+    x[:, ::3000] *= 1e5
+    y, mean, rstd = pkg.group_norm_act(x, 32, act="silu")
+    dx, *_ = pkg.group_norm_act_backward(x, x, mean, rstd, 32, act="silu")
+    for i in (0, 150, 299):
+        one, m, r = x[i:i + 1], mean[i:i + 1], rstd[i:i + 1]
+        check_forward(one, 32, None, None, "silu", None, None, got=(y[i:i + 1], m, r))
+        check_backward(one, one, m, r, 32, None, None, "silu", None, None, got=(dx[i:i + 1], None, None, None, None))
+
+
+def test_more_than_2_to_the_40_values_are_refused():
+    L = Bd.load()
+    for B, ok in ((1 << 10, False), ((1 << 10) - 1, True)):
+        p = norm(B=B, T=1 << 20, C=1 << 10, groups=1)
+        assert (L.mh3a_group_norm_act_workspace(C.byref(p), 0, 0) > 0) == ok
