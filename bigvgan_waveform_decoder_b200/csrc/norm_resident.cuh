@@ -111,29 +111,42 @@ __device__ __forceinline__ F warp_sum(F v) {
     return v;
 }
 
-// The block's statistics of one group (the result is in all lanes of the warp): entries (row of
-// threads, first .. first + span) of `part`, a few per lane, put together in fp64.
-__device__ __forceinline__ Part group_stats(const Part* part, int ty_n, int width, int first, FastDiv span) {
-    const int lane = threadIdx.x & 31, m = ty_n * span.d;
-    float n = 0.f;
-    double s = 0.0;
+// Where the threads' statistics lie: rows of threads by vectors, or by channels, those of one place in the
+// vector side by side (a thread that stored its channels one behind the other would meet the banks of
+// its neighbours: 1900 cycles against 100 for 200 channels).
+template <int V, bool WHOLE>
+__device__ __forceinline__ int part_index(int row, int i, int w) {
+    return WHOLE ? row * w + i : (row * V + i % V) * w + i / V;
+}
+
+// The block's statistics of one group (the result is in all lanes of the warp), from `rows` rows of threads
+// and the entries first .. first + span of each, about the first one's mean, in fp64: one pass, and nothing
+// to lose but its distance from the group's mean, squared, in 53 bits.  inv = 1 / n.
+template <int V, bool WHOLE>
+__device__ __forceinline__ Part group_stats(const Part* part, int rows, int w, int first, FastDiv span, float n, double inv) {
+    const int lane = threadIdx.x & 31, m = rows * span.d;
+    const Part ref = part[part_index<V, WHOLE>(0, first, w)];
+    double s = 0.0, q = 0.0;
+    float m2 = 0.f;
+#pragma unroll 4
     for (int i = lane; i < m; i += 32) {
         const int row = (unsigned)i / span;
-        const Part v = part[row * (width - (int)span.d) + first + i];
-        n += v.n;
-        if (v.n > 0.f) s += ((double)v.hi + (double)v.lo) * v.n;
+        const Part v = part[part_index<V, WHOLE>(row, first + i - row * (int)span.d, w)];
+        const double d = (v.hi - ref.hi) + (v.lo - ref.lo), nd = d * v.n;
+        s += nd;
+        q = fma(nd, d, q);
+        m2 += v.m2;
     }
-    n = warp_sum(n);
-    const double mean = n > 0.f ? warp_sum(s) / n : 0.0;
-    double q = 0.0;
-    for (int i = lane; i < m; i += 32) {
-        const int row = (unsigned)i / span;
-        const Part v = part[row * (width - (int)span.d) + first + i];
-        const double d = (double)v.hi + (double)v.lo - mean;
-        if (v.n > 0.f) q += fma(v.n * d, d, (double)v.m2);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, off);
+        q += __shfl_xor_sync(0xffffffffu, q, off);
+        m2 += __shfl_xor_sync(0xffffffffu, m2, off);
     }
+    if (!(n > 0.f)) return Part{0.f, 0.f, 0.f, 0.f};
+    const double d = s * inv, mean = (double)ref.hi + ((double)ref.lo + d);
     const float hi = (float)mean;
-    return Part{hi, (float)(mean - hi), (float)warp_sum(q), n};
+    return Part{hi, (float)(mean - hi), (float)(m2 + (q - s * d)), n};
 }
 
 // WHOLE: no vector straddles two groups (D is a multiple of V).
@@ -153,7 +166,6 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
     float2* fin = reinterpret_cast<float2*>(bar + 2);  // (mean, rstd)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int next = p.TY * p.w;  // between a thread's rows in shared memory, in vectors
-    const int width = WHOLE ? p.w : r.W;
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar, 1);
         ptx::fence_mbar_init();
@@ -191,6 +203,8 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
             for (int i = 0; i < H; ++i) ib[i] = make_float2(rcp_ftz(ib[i].x + 1e-9f), rcp_ftz(ib[i].y + 1e-9f));
         }
     }
+    const float group_n = (float)have * a.D;  // the group's values here, and what they are divided by, here and in all
+    const double inv_here = have > 0 ? 1.0 / ((double)have * a.D) : 0.0, inv_count = n > 0 ? 1.0 / ((double)n * a.D) : 0.0;
     const Pack<T, V>* mydata = reinterpret_cast<const Pack<T, V>*>(smem) + p.tx + p.ty * p.w;
 
     // Sums of deviations from a value near the thread's mean: the mean of its first rows.  An
@@ -236,20 +250,20 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
         const float cnt = (float)(WHOLE ? mine * V : mine), ic = mine > 0 ? rcp_ftz(cnt) : 0.f;
         if (WHOLE) {
             const float sum = s[0].x + s[0].y, lo = sum * ic;
-            part[p.ty * width + p.tx] = Part{-sh[0].x, lo, q[0].x + q[0].y - sum * lo, cnt};
+            part[p.ty * p.w + p.tx] = Part{-sh[0].x, lo, q[0].x + q[0].y - sum * lo, cnt};
         } else {
-            Part* to = part + p.ty * width + p.tx * V;
+            Part* to = part + p.ty * r.W + p.tx;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                to[2 * i] = Part{-sh[i].x, s[i].x * ic, q[i].x - s[i].x * s[i].x * ic, cnt};
-                to[2 * i + 1] = Part{-sh[i].y, s[i].y * ic, q[i].y - s[i].y * s[i].y * ic, cnt};
+                to[2 * i * p.w] = Part{-sh[i].x, s[i].x * ic, q[i].x - s[i].x * s[i].x * ic, cnt};
+                to[(2 * i + 1) * p.w] = Part{-sh[i].y, s[i].y * ic, q[i].y - s[i].y * s[i].y * ic, cnt};
             }
         }
     }
     __syncthreads();
     cluster_wait();  // the peers' mbarriers are initialised
     for (int g = warp; g < ng; g += kResThreads / 32) {
-        const Part o = group_stats(part, p.TY, width, g * r.span.d, r.span);
+        const Part o = group_stats<V, WHOLE>(part, min(p.TY, have), p.w, g * r.span.d, r.span, group_n, inv_here);
         if (lane < r.S)
             send16(peer_smem(ptx::smem_u32(inbox + p.rank * ng + g), lane), peer_smem(ptx::smem_u32(bar), lane),
                    make_float4(o.hi, o.lo, o.m2, o.n));
@@ -258,19 +272,20 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
     for (int g = warp; g < ng; g += kResThreads / 32) {
         Part o{0.f, 0.f, 0.f, 0.f};
         if (lane < r.S) o = inbox[lane * ng + g];
-        if (!arrived) o.m2 = __int_as_float(0x7fffffff);  // never expected: NaN rather than stale sums
-        const double inv_count = n > 0 ? 1.0 / ((double)n * a.D) : 0.0;
-        const double m = (double)o.hi + (double)o.lo;
-        double sum = o.n > 0.f ? m * o.n : 0.0;
+        const Part ref = inbox[g];  // the first block has rows if any has
+        const double from = (double)(o.hi - ref.hi) + (double)o.lo;
+        double s1 = o.n > 0.f ? from * o.n : 0.0, s2 = o.n > 0.f ? fma(s1, from, (double)o.m2) : 0.0;
 #pragma unroll
-        for (int off = 8; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        const double mean = sum * inv_count, d = m - mean;
-        double m2 = o.n > 0.f ? (double)o.m2 + d * d * o.n : 0.0;
-#pragma unroll
-        for (int off = 8; off; off >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, off);
+        for (int off = 8; off; off >>= 1) {
+            s1 += __shfl_xor_sync(0xffffffffu, s1, off);
+            s2 += __shfl_xor_sync(0xffffffffu, s2, off);
+        }
         if (lane == 0) {
-            // equal values leave a sum of squares within rounding of 0, on either side (NaN stays)
-            const float rstd = 1.0f / sqrtf((float)((m2 < 0.0 ? 0.0 : m2 * inv_count) + (double)a.eps));
+            const double d = s1 * inv_count, mean = (double)ref.hi + d, var = s2 * inv_count - d * d;
+            // Equal values leave a variance within rounding of 0, on either side (NaN stays).  A wait that ran
+            // out of time, never expected, gives NaN rather than stale sums.
+            const float root = sqrtf((float)((var < 0.0 ? 0.0 : var) + (double)a.eps));
+            const float rstd = arrived ? 1.0f / root : __int_as_float(0x7fffffff);
             fin[g] = make_float2((float)mean, rstd);
             if (p.rank == 0) {
                 const long long at = (long long)p.b * a.G + p.c0 / a.D + g;
