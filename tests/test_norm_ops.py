@@ -472,3 +472,27 @@ def test_more_than_2_to_the_40_values_are_refused():
     for B, ok in ((1 << 10, False), ((1 << 10) - 1, True)):
         p = norm(B=B, T=1 << 20, C=1 << 10, groups=1)
         assert (L.mh3a_group_norm_act_workspace(C.byref(p), 0, 0) > 0) == ok
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp16", "bf16"))
+@pytest.mark.parametrize("T", (40, 70000))
+def test_silu_far_out(T, dtype):
+    """Arguments from the exponential's overflow to its underflow, infinities and NaN, in both places of a pair."""
+    Cn = 32
+    x = case(1, T, Cn, "none", dtype, seed=3)[0]
+    b = torch.linspace(-140, 140, Cn, device="cuda")
+    for shift in (0, 1):
+        b = b.roll(shift)
+        y, mean, rstd = check_forward(x, 4, None, b, "silu", None, None)
+        check_backward(x, x, mean, rstd, 4, None, b, "silu", None, None)
+        far = b.clone()
+        far[:3] = torch.tensor([float("inf"), -float("inf"), float("nan")])
+        far[5], far[6] = float("nan"), -float("inf")
+        got = pkg.group_norm_act(x, 4, None, far, act="silu")[0]
+        odd = torch.tensor([0, 1, 2, 5, 6], device="cuda")
+        rest = torch.tensor([i for i in range(Cn) if i not in (0, 1, 2, 5, 6)], device="cuda")
+        assert torch.equal(got[..., rest], y[..., rest])
+        assert torch.all(got[..., 0] == float("inf")) and torch.isnan(got[..., odd[2:4]]).all()
+        # -inf times a sigmoid of 0, or of 2^-126 where it is clamped there: never a finite number
+        assert not torch.isfinite(got[..., odd[[1, 4]]]).any()
