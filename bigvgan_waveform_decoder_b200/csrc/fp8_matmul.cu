@@ -37,7 +37,7 @@ struct MatmulParams {
     int M, N, KB, NB;
     int mt, tiles;      // row tiles, all tiles
     int vec_out;        // rows of `out` can be written 16 bytes at a time
-    int stage_bytes;    // what the two copies of a step bring
+    int step_bytes;     // what the two copies of a step bring
 };
 
 template <int NT>
@@ -52,7 +52,11 @@ struct Cfg {
     static constexpr int kCols = kAcc * kStep * NT;
     static constexpr int kAhead = kStep == 1 ? 3 : 2 * kStep;  // steps that scales are fetched ahead
     static constexpr int kScaleSlots = kStep == 1 ? 4 : 2 * kStep;
-    static constexpr int kStageBytes = (kM + NT) * kBlock;
+    // Steps of K in one stage of shared memory: their copies are announced, waited for and given back
+    // together, since each of these costs the issuing warp 60 to 150 cycles.
+    static constexpr int kPer = NT == 256 ? 1 : 2;
+    static constexpr int kStepBytes = (kM + NT) * kBlock;
+    static constexpr int kStageBytes = kPer * kStepBytes;
     static constexpr int kStaging = EW * 32 * kPitch;
     static constexpr int kOther = kStaging + kScaleSlots * NT * 4 + 1024 + 512;
     static constexpr int kStages = std::min(8, (227 * 1024 - kOther) / kStageBytes);
@@ -60,6 +64,19 @@ struct Cfg {
     // 128 columns of sums and two buffers of 32 do not fit an even share of the registers
     static constexpr bool kSplitRegs = CW == 128;
 };
+
+// Whether a barrier's phase has completed, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(ptx::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok;
+}
 
 // The thread's earlier cp.async copies count as one arrival on the barrier once they are done.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -217,7 +234,7 @@ template <typename O, int NT, bool WIDE>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
 k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
     using C = Cfg<NT>;
-    constexpr int kStep = C::kStep, kAhead = C::kAhead, kScaleSlots = C::kScaleSlots;
+    constexpr int kStep = C::kStep, kPer = C::kPer, kAhead = C::kAhead, kScaleSlots = C::kScaleSlots;
     extern __shared__ unsigned char raw[];
     unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     unsigned char* staging = tiles + C::kStages * C::kStageBytes;
@@ -269,14 +286,20 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
             bool ok = true;
             for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
                 const int m0 = (t % p.mt) * kM, n0 = (t / p.mt) * NT;
-                for (int kb = 0; kb < p.KB; ++kb, ++it) {
+                for (int kb = 0; kb < p.KB; kb += kPer, ++it) {
                     const int s = it % C::kStages;
                     if (it >= C::kStages) ok = ptx::mbar_wait(empty + s, ((it / C::kStages) & 1) ^ 1);
                     if (!ok) break;
                     unsigned char* to = tiles + s * C::kStageBytes;
-                    ptx::mbar_arrive_expect_tx(full + s, p.stage_bytes);
-                    tma_load_2d(to, &map_a, kb * kBlock, m0, full + s);
-                    tma_load_2d(to + kM * kBlock, &map_b, kb * kBlock, n0, full + s);
+                    const int steps = kPer == 1 ? 1 : min(kPer, p.KB - kb);
+                    ptx::mbar_arrive_expect_tx(full + s, steps * p.step_bytes);
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) {
+                        if (j < steps) {
+                            tma_load_2d(to + j * C::kStepBytes, &map_a, (kb + j) * kBlock, m0, full + s);
+                            tma_load_2d(to + j * C::kStepBytes + kM * kBlock, &map_b, (kb + j) * kBlock, n0, full + s);
+                        }
+                    }
                 }
             }
             // never expected: after a wait that ran out of time, the copies on their way are seen in
@@ -284,25 +307,35 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                 for (int j = max(0, it - C::kStages); j < it; ++j) ptx::mbar_wait(full + j % C::kStages, (j / C::kStages) & 1);
         } else if (warp == 1) {
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);  // e4m3, fp32 sums
-            int it = 0, round = 0;
-            bool ok = true;
+            int it = 0, round = 0, column = 0;  // stages, handshakes, steps with column scales
+            bool ok = true, there = false;  // there: the next stage's copies are known to have arrived
             for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
                 for (int k0 = 0; k0 < p.KB && ok; k0 += kStep, ++round) {
-                    const int b = round % C::kAcc, steps = kStep == 1 ? 1 : min(kStep, p.KB - k0), it0 = it;
+                    const int b = round % C::kAcc, steps = kStep == 1 ? 1 : min(kStep, p.KB - k0);
                     if (round >= C::kAcc) ok = ptx::mbar_wait(freed + b, ((round / C::kAcc) & 1) ^ 1);
-                    for (int j = 0; j < steps && ok; ++j, ++it) {
+#pragma unroll
+                    for (int j = 0; j < kStep; j += kPer) {
+                        if (j >= steps || !ok) break;
                         const int s = it % C::kStages;
-                        ok = ptx::mbar_wait(full + s, (it / C::kStages) & 1);
+                        if (!there) ok = ptx::mbar_wait(full + s, (it / C::kStages) & 1);
                         if (!ok) break;
+                        ++it;
+                        there = __all_sync(0xffffffffu, mbar_test(full + it % C::kStages, (it / C::kStages) & 1));
                         ptx::tc_fence_after();
                         const uint32_t at = ptx::smem_u32(tiles + s * C::kStageBytes);
-                        mma_block_elect(tmem + (b * kStep + j) * NT, desc_sw128(at), desc_sw128(at + kM * kBlock), idesc);
+#pragma unroll
+                        for (int i = 0; i < kPer; ++i) {
+                            if (i == 0 || j + i < steps)
+                                mma_block_elect(tmem + (b * kStep + j + i) * NT, desc_sw128(at + i * C::kStepBytes),
+                                                desc_sw128(at + i * C::kStepBytes + kM * kBlock), idesc);
+                        }
                         ptx::mma_commit_elect(empty + s);
                     }
                     if (!ok) break;
                     ptx::mma_commit_elect(done + b);
                     if (!WIDE) {
-                        for (int i = it0; i < it; ++i) ok = ok && ptx::mbar_wait(sfull + i % kScaleSlots, (i / kScaleSlots) & 1);
+                        for (int i = 0; i < steps; ++i, ++column)
+                            ok = ok && ptx::mbar_wait(sfull + column % kScaleSlots, (column / kScaleSlots) & 1);
                         if (lane == 0) ptx::mbar_arrive(done + b);
                     }
                 }
@@ -531,7 +564,7 @@ int launch(const MatmulArgs& m, cudaStream_t s) {
     // results that are not written.  (Boxes of 128 rows of a matrix of 9 to 15: 29 us, 16 rows and more 19,
     // at 8192 x 8192.)
     const int a_rows = std::min(m.M, kM), b_rows = std::min(m.N, NT);
-    p.stage_bytes = (a_rows + b_rows) * kBlock;
+    p.step_bytes = (a_rows + b_rows) * kBlock;
     CUtensorMap ma, mb;
     if (!make_map(&ma, m.a, m.M, m.K, m.as, a_rows) || !make_map(&mb, m.b, m.N, m.K, m.bs, b_rows)) return -1;
     auto kern = k_fp8_matmul<O, NT, WIDE>;
