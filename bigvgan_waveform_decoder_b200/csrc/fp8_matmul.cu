@@ -457,8 +457,8 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                         }
                     } else {
                         // Column scales: a lane of the fragments needs a quarter of them, where a lane that holds a
-                        // whole row would read all from shared memory, 512 bytes a load and four columns (74 us
-                        // against 66 at 2048 x 2048 x 6400 in tiles of 128 columns).
+                        // whole row would read all from shared memory, 512 bytes a load and four columns (12 %
+                        // slower at 2048 x 2048 x 6400 in tiles of 128 columns).
                         uint32_t v[2][2][kLd / 2];
                         auto load = [&](int c) {
                             const uint32_t from = buf + c / kPieces * NT + c % kPieces * kLd;
@@ -575,10 +575,11 @@ int launch(const MatmulArgs& m, cudaStream_t s) {
 
 template <typename O, bool WIDE>
 int launch_nt(const MatmulArgs& m, cudaStream_t s) {
-    // Rounds of tiles over the SMs, times what a round takes with tiles of that width (relative, from
-    // K = 2048: 8.5, 5.6, 4.1, 3.4 and 3.0 us).  Measured there, us with 256 / 128 / 64 / 32 / 16 columns:
-    // 64 x 2048: 11.1 / 8.0 / 6.8 / 6.3 / 5.9; 800 x 1024: 11.7 / 8.6 / 7.2 / 10.6 / 17.6; 800 x 2048: 12.0 /
-    // 9.2 / 12.0 / 18.8 / 29.6; 2048 x 2048: 12.9 / 16.0 / 21.9 / 31.7 / 57.5.
+    // Rounds of tiles over the SMs, times what a round takes with tiles of that width (relative; measured
+    // at K = 2048: 9.4, 6.0, 3.7, 3.1 and 3.1 us, of one round 0.2 us less with 16 columns than with 32).
+    // Measured there, us with 256 / 128 / 64 / 32 / 16 columns: 64 x 2048: 10.6 / 7.4 / 5.9 / 5.5 / 5.3; 800 x
+    // 1024: 11.9 / 8.2 / 6.8 / 9.0 / 14.5; 800 x 2048: 12.1 / 8.6 / 10.4 / 15.1 / 23.3; 2048 x 2048: 12.9 / 14.5 /
+    // 17.8 / 24.6 / 44.6.
     const long long mt = (m.M + kM - 1LL) / kM;
     auto cost = [&](int nt, long long round) { return (mt * ((m.N + nt - 1LL) / nt) + kSms - 1) / kSms * round; };
     const long long c256 = cost(256, 17), c128 = cost(128, 11), c64 = cost(64, 8), c32 = cost(32, 7), c16 = cost(16, 6);

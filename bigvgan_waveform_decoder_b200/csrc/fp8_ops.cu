@@ -170,10 +170,10 @@ bool stored_ok(const void* q, long long stride, int cols) {
 long long blocks(int n) { return (n + (long long)kBlock - 1) / kBlock; }
 
 // Whether a layer takes the kernel for few rows; its multiplications are the CUDA cores', so the tensor
-// cores overtake it where there are many.  Measured, us, this kernel against quantisation and product:
-// 1 row 2048 x 2048 3.4 / 6.9, 2048 x 8192 7.0 / 8.1, 8192 x 8192 25.7 / 20.7; 2 rows 4096 x 4096 7.7 / 11.0;
-// 4 rows 2048 x 2048 5.2 / 6.9, 4096 x 4096 12.0 / 11.1, 8192 x 8192 42.2 / 21.1.
-bool few_rows(int M, int N, int K) { return M <= MH3A_FP8_FEW_ROWS && (long long)M * N * K <= 48LL << 20; }
+// cores overtake it where there are many.  Measured, us, this kernel against quantisation and product
+// (columns x K): 1 row 2048 x 2048 3.4 / 6.3, 4096 x 4096 6.7 / 9.7, 8192 x 8192 25.7 / 16.7; 2 rows 4096 x 4096
+// 7.7 / 9.8; 3 rows 4096 x 4096 11.3 / 9.8; 4 rows 2048 x 2048 5.0 / 6.6.
+bool few_rows(int M, int N, int K) { return M <= MH3A_FP8_FEW_ROWS && (long long)M * N * K <= 40LL << 20; }
 
 // Layout of mh3a_fp8_linear's scratch: x quantised, then its scales.
 long long q_stride(int K) { return (K + 15LL) / 16 * 16; }
