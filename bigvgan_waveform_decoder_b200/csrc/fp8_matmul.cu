@@ -471,17 +471,19 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                             const int j = c / kPieces, next = c + 1;
                             if (FULL || j < count) {
                                 const float* cs = scales + (it + j) % kScaleSlots * NT + half * C::CW + 2 * (lane & 3);
+                                float2 k2[kLd / 8];  // while the sums are on their way
+#pragma unroll
+                                for (int i = 0; i < kLd / 8; ++i) k2[i] = *reinterpret_cast<const float2*>(cs + c % kPieces * kLd + 8 * i);
                                 tmem_wait(v[c & 1][0]);
                                 tmem_wait(v[c & 1][1]);
                                 if (next < count * kPieces) load(next);
                                 else hand_back();
 #pragma unroll
                                 for (int i = 0; i < kLd / 8; ++i) {
-                                    const float2 k2 = *reinterpret_cast<const float2*>(cs + c % kPieces * kLd + 8 * i);
 #pragma unroll
                                     for (int r = 0; r < 4; ++r) {
                                         const uint32_t* w = &v[c & 1][r / 2][4 * i + 2 * (r % 2)];
-                                        const float2 f = __fmul2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), k2);
+                                        const float2 f = __fmul2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), k2[i]);
                                         float2& to = acc[(c % kPieces * kLd / 8 + i) * 4 + r];
                                         to = __ffma2_rn(f, make_float2(s1[j][r], s1[j][r]), to);
                                     }
