@@ -83,8 +83,9 @@ __device__ __forceinline__ void send16(uint32_t to, uint32_t bar, float4 v) {
                  "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
                  : "memory");
 }
-// Waits (up to a second) for the bytes that the peers send to this block's mbarrier.
-__device__ __forceinline__ bool wait_for_peers(uint64_t* bar) {
+// Waits (up to a second) for the bytes that the peers send to this block's mbarrier.  A thread whose wait
+// succeeded may read the inbox; a thread that gave up must not use it.
+__device__ __forceinline__ bool wait_for_peers(uint64_t* bar, uint64_t limit_ns = 1000000000ull) {
     const uint64_t t0 = ptx::globaltimer_ns();
     for (;;) {
         for (int i = 0; i < 64; ++i) {
@@ -98,11 +99,23 @@ __device__ __forceinline__ bool wait_for_peers(uint64_t* bar) {
                 : "memory");
             if (ok) return true;
         }
-        if (ptx::globaltimer_ns() - t0 > 1000000000ull) return false;
+        if (ptx::globaltimer_ns() - t0 > limit_ns) return false;
     }
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The end of a block, `arrived` the same in all its threads.  After a wait that succeeded nothing is on its way
+// to this block any more.  After one that was given up (never expected) the block's shared memory has to
+// outlive what the peers still send: it stays until every peer has ended or has come here too (each within
+// limits of its own; the barrier does not count blocks that have ended), and what they sent has landed.
+__device__ __forceinline__ void leave_peers(bool arrived, uint64_t* bar, uint64_t limit_ns = 1000000000ull) {
+    if (arrived) return;
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    wait_for_peers(bar, limit_ns);
+}
 
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
@@ -268,7 +281,7 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
             send16(peer_smem(ptx::smem_u32(inbox + p.rank * ng + g), lane), peer_smem(ptx::smem_u32(bar), lane),
                    make_float4(o.hi, o.lo, o.m2, o.n));
     }
-    const bool arrived = wait_for_peers(bar);  // so no peer sends to this block after it has ended
+    const bool arrived = wait_for_peers(bar);
     for (int g = warp; g < ng; g += kResThreads / 32) {
         Part o{0.f, 0.f, 0.f, 0.f};
         if (lane < r.S) o = inbox[lane * ng + g];
@@ -284,17 +297,17 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
             const double d = s1 * inv_count, mean = (double)ref.hi + d, var = s2 * inv_count - d * d;
             // Equal values leave a variance within rounding of 0, on either side (NaN stays).  A wait that ran
             // out of time, never expected, gives NaN rather than stale sums.
-            const float root = sqrtf((float)((var < 0.0 ? 0.0 : var) + (double)a.eps));
-            const float rstd = arrived ? 1.0f / root : __int_as_float(0x7fffffff);
-            fin[g] = make_float2((float)mean, rstd);
+            const float root = sqrtf((float)((var < 0.0 ? 0.0 : var) + (double)a.eps)), nan = __int_as_float(0x7fffffff);
+            const float2 f = arrived ? make_float2((float)mean, 1.0f / root) : make_float2(nan, nan);
+            fin[g] = f;
             if (p.rank == 0) {
                 const long long at = (long long)p.b * a.G + p.c0 / a.D + g;
-                a.mean[at] = (float)mean;
-                a.rstd[at] = rstd;
+                a.mean[at] = f.x;
+                a.rstd[at] = f.y;
             }
         }
     }
-    __syncthreads();
+    const bool all_arrived = __syncthreads_and(arrived);
 
     if (p.live) {
         float2 mu[H], sc[H];
@@ -322,6 +335,7 @@ __global__ void __launch_bounds__(kResThreads) k_norm_resident(const NormArgs a,
         const Pack<T, V> zero{};  // rows behind the item's length
         for (int k = mine; p.ty + k * p.TY < r1 - r0; ++k, y += step) *reinterpret_cast<Pack<T, V>*>(y) = zero;
     }
+    leave_peers(all_arrived, bar);
 }
 
 // Backward: shared memory behind x and dy: the threads' per-channel sums (one row for each warp where
@@ -477,7 +491,7 @@ __global__ void __launch_bounds__(kResThreads) k_norm_bwd_resident(const NormArg
         for (int k = 0; k < r.S; ++k) s += inbox[k * cols + c];
         total[c] = arrived ? s : __int_as_float(0x7fffffff);
     }
-    __syncthreads();
+    const bool all_arrived = __syncthreads_and(arrived);
     for (int g = warp; g < ng; g += kResThreads / 32) {
         float s1 = 0.f, s2 = 0.f;
         for (int i = lane; i < a.D; i += 32) {
@@ -544,6 +558,7 @@ __global__ void __launch_bounds__(kResThreads) k_norm_bwd_resident(const NormArg
         const Pack<T, V> zero{};
         for (; p.ty + k * p.TY < r1 - r0; ++k, dx += step) *reinterpret_cast<Pack<T, V>*>(dx) = zero;
     }
+    leave_peers(all_arrived, bar);
 }
 
 }  // namespace norm
