@@ -25,6 +25,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// A wait by a whole warp, the same answer in all lanes: what follows has to be done by all or by none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns = 1000000000ull) {
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, limit_ns));
+}
+
 template <typename T>
 __device__ __forceinline__ float as_float(T v);
 template <>

@@ -245,7 +245,7 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
     uint64_t* freed = done + C::kAcc;     // and read again
     uint64_t* sfull = freed + C::kAcc;    // scales of a step are there
     uint64_t* sempty = sfull + kScaleSlots;
-    uint64_t* drain = sempty + kScaleSlots;  // only after a wait that ran out of time
+    uint64_t* drain = sempty + kScaleSlots;  // the last MMAs
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -302,9 +302,8 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                     }
                 }
             }
-            // never expected: after a wait that ran out of time, the copies on their way are seen in
-            if (!ok)
-                for (int j = max(0, it - C::kStages); j < it; ++j) ptx::mbar_wait(full + j % C::kStages, (j / C::kStages) & 1);
+            // the block's shared memory outlives the copies on their way, also where another warp gave up
+            for (int j = max(0, it - C::kStages); j < it; ++j) ptx::mbar_wait(full + j % C::kStages, (j / C::kStages) & 1);
         } else if (warp == 1) {
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);  // e4m3, fp32 sums
             int it = 0, round = 0, column = 0;  // stages, handshakes, steps with column scales
@@ -312,12 +311,12 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
             for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
                 for (int k0 = 0; k0 < p.KB && ok; k0 += kStep, ++round) {
                     const int b = round % C::kAcc, steps = kStep == 1 ? 1 : min(kStep, p.KB - k0);
-                    if (round >= C::kAcc) ok = ptx::mbar_wait(freed + b, ((round / C::kAcc) & 1) ^ 1);
+                    if (round >= C::kAcc) ok = warp_wait(freed + b, ((round / C::kAcc) & 1) ^ 1);
 #pragma unroll
                     for (int j = 0; j < kStep; j += kPer) {
                         if (j >= steps || !ok) break;
                         const int s = it % C::kStages;
-                        if (!there) ok = ptx::mbar_wait(full + s, (it / C::kStages) & 1);
+                        if (!there) ok = warp_wait(full + s, (it / C::kStages) & 1);
                         if (!ok) break;
                         ++it;
                         there = __all_sync(0xffffffffu, mbar_test(full + it % C::kStages, (it / C::kStages) & 1));
@@ -335,15 +334,14 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                     ptx::mma_commit_elect(done + b);
                     if (!WIDE) {
                         for (int i = 0; i < steps; ++i, ++column)
-                            ok = ok && ptx::mbar_wait(sfull + column % kScaleSlots, (column / kScaleSlots) & 1);
-                        if (lane == 0) ptx::mbar_arrive(done + b);
+                            ok = ok && warp_wait(sfull + column % kScaleSlots, (column / kScaleSlots) & 1);
+                        if (ok && lane == 0) ptx::mbar_arrive(done + b);
                     }
                 }
             }
-            if (!ok) {  // the MMAs on their way end before tensor memory is given back
-                ptx::mma_commit_elect(drain);
-                ptx::mbar_wait(drain, 0);
-            }
+            // the MMAs on their way end before tensor memory is given back, also where another warp gave up
+            ptx::mma_commit_elect(drain);
+            warp_wait(drain, 0);
         } else if (warp == 2 && !WIDE) {
             int it = 0;
             bool ok = true;
@@ -351,7 +349,7 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                 const int n0 = (t / p.mt) * NT;
                 for (int kb = 0; kb < p.KB; ++kb, ++it) {
                     const int s = it % kScaleSlots;
-                    if (it >= kScaleSlots) ok = ptx::mbar_wait(sempty + s, ((it / kScaleSlots) & 1) ^ 1);
+                    if (it >= kScaleSlots) ok = warp_wait(sempty + s, ((it / kScaleSlots) & 1) ^ 1);
                     if (!ok) break;
                     float* to = scales + s * NT;
                     const float* sb = p.sb + (long long)kb * p.NB;
@@ -361,12 +359,16 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                     cp_async_arrive(sfull + s);
                 }
             }
+            ptx::cp_async_wait_all();
         }
     } else {
         if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int e = warp - 4, quarter = warp & 3, half = e >> 2;
         const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::CW;
         int it = 0, round = 0;  // steps with column scales; handshakes
+        // A warp whose wait ran out of time, never expected, hands nothing back any more: the warps it works with
+        // then run into limits of their own instead of over data that others still read.
+        bool ok = true;
         for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
             const int m0 = (t % p.mt) * kM + quarter * 32, n0 = (t / p.mt) * NT + half * C::CW;
             float2 acc[C::CW / 2];
@@ -406,8 +408,7 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
             };
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) fetch(i, i);
-            bool ok = true;
-            for (int k0 = 0; k0 < p.KB; k0 += kStep, ++round) {
+            for (int k0 = 0; k0 < p.KB && ok; k0 += kStep, ++round) {
                 const int b = round % C::kAcc, steps = kStep == 1 ? 1 : min(kStep, p.KB - k0);
                 float s1[kStep][kRows];
 #pragma unroll
@@ -422,7 +423,8 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                 }
 #pragma unroll
                 for (int j = 0; j < kStep; ++j) fetch(kAhead - kStep + j, k0 + kAhead + j);
-                ok = ok && ptx::mbar_wait(done + b, (round / C::kAcc) & 1);
+                ok = warp_wait(done + b, (round / C::kAcc) & 1);
+                if (!ok) break;
                 ptx::tc_fence_after();
                 // the next columns are on their way while a piece is added up
                 constexpr int kLd = C::CW >= 32 ? 32 : 16, kPieces = C::CW / kLd;
@@ -501,7 +503,7 @@ k_fp8_matmul(const MatmulParams p, const __grid_constant__ CUtensorMap map_a, co
                     it += steps;
                 }
             }
-            if (!ok) {  // never expected: a wait ran out of time; NaN rather than a partial sum
+            if (!ok) {  // NaN rather than a partial sum
 #pragma unroll
                 for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
             }

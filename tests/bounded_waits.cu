@@ -2,6 +2,7 @@
 //
 // What a wait is for comes late or never here, because a thread of the test holds it back; every limit is
 // milliseconds.  The kernels only use the library's own waiting code, and report what it answered.
+#include "fp8_kernels.cuh"
 #include "norm_resident.cuh"
 
 using namespace mh3a;
@@ -42,7 +43,32 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(256) k_peers(int sl
     if (lane < kCluster) out[kCluster + rank * kCluster + lane] = (int)inbox[lane].x;
 }
 
+// The first warp waits on a barrier that the second completes after 100 ms; its even lanes would wait a second,
+// its odd ones give up after a millisecond.
+__global__ void __launch_bounds__(64) k_warp(int* out) {
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&bar, 1);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        out[threadIdx.x] = fp8::warp_wait(&bar, 0, threadIdx.x % 2 ? 1000000 : 1000000000);
+        out[32 + threadIdx.x] = fp8::warp_wait(&bar, 0);
+    } else if (threadIdx.x == 32) {
+        hold(100000000);
+        ptx::mbar_arrive(&bar);
+    }
+}
+
 }  // namespace
+
+// `out`: device, 64 values: the lanes' answers of the wait that some of them give up, and of one after it.
+extern "C" __attribute__((visibility("default"))) int run_warp(int* out) {
+    k_warp<<<1, 64>>>(out);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : cudaDeviceSynchronize();
+}
 
 // `out`: device, 20 values.  The CUDA error of the launch and its end.
 extern "C" __attribute__((visibility("default"))) int run_peers(int slow, int never, int* out) {

@@ -44,3 +44,11 @@ def test_a_cluster_without_a_late_peer_does_not_give_up(waits):
     out = torch.full((20,), -1, dtype=torch.int32, device="cuda")
     assert waits.run_peers(-1, 0, C.c_void_p(out.data_ptr())) == 0
     assert out[:4].tolist() == [1] * 4 and out[4:].view(4, 4).tolist() == [[1, 2, 3, 4]] * 4
+
+
+@pytest.mark.gpu
+def test_a_warp_gives_up_together(waits):
+    """Lanes whose limits run out at different times get one answer, so that no lane goes on alone."""
+    out = torch.full((64,), -1, dtype=torch.int32, device="cuda")
+    assert waits.run_warp(C.c_void_p(out.data_ptr())) == 0
+    assert out.tolist() == [0] * 32 + [1] * 32
