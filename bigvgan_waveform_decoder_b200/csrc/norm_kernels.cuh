@@ -208,17 +208,11 @@ __device__ __forceinline__ float rcp_ftz(float x) {
     return y;
 }
 
-// The smaller of two values; NaN stays NaN.
-__device__ __forceinline__ float min_nan(float v, float c) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(c));
-    return r;
-}
-
-// 1 / x for x in [1, 2^127): a first guess by taking x's bits (exponent and fraction, so a piecewise linear
-// logarithm) from a constant, then a step of Newton's iteration and one of third order for what is
-// left.  The constant minimises the guess's largest relative error, 0.051 (by search); then 2.6e-3, then
-// 1.7e-8, below the roundings.
+// 1 / x for x in [1, 2^126]: a first guess by taking x's bits (exponent and fraction, so a piecewise linear
+// logarithm) from a constant, then a step of Newton's iteration and one of third order for what is left.
+// The constant minimises the guess's largest relative error, 0.051 (by search); then 2.6e-3, then 1.7e-8,
+// below the roundings (8e-8 in all).  From 2^125.9 on the guess is no normal number any more, which leaves
+// 1.2e-6 at 2^126; beyond 1.9 2^126 the subtraction gives no number at all.
 __device__ __forceinline__ float rcp_newton(float x) {
     float y = __uint_as_float(0x7ef31000u - __float_as_uint(x));
     y = fmaf(y, fmaf(-x, y, 1.f), y);
@@ -229,14 +223,14 @@ __device__ __forceinline__ float rcp_newton(float x) {
 // 1 / (1 + e^-u).  16-bit tensors take the hardware's exponential and reciprocal (each a few ulp;
 // results below 2^-126 become 0), without the scaling that keeps subnormal numbers, but for one of
 // the two reciprocals: the unit that computes these takes eight cycles for a warp, and three of them beside
-// five multiplications take less time than four (7 items of [3001, 200] 9.36 us with none, 8.72 with one,
-// 8.91 with both by multiplications).
+// five multiplications take less time than four (7 items of [3001, 200] 9.36 us with both by the unit, 9.11
+// with one).  The two channels of a pair so differ by a few units of 2^-24 for equal u, and nowhere else.
 template <bool PRECISE>
 __device__ __forceinline__ float2 sigmoid(float2 u) {
     if (PRECISE) return make_float2(1.0f / (1.0f + expf(-u.x)), 1.0f / (1.0f + expf(-u.y)));
     const float2 t = __fmul2_rn(u, both(-1.44269504088896341f));
-    const float2 e = __fadd2_rn(make_float2(ex2_ftz(t.x), ex2_ftz(min_nan(t.y, 126.f))), both(1.f));
-    return make_float2(rcp_ftz(e.x), rcp_newton(e.y));
+    const float2 e = __fadd2_rn(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), both(1.f));
+    return make_float2(rcp_ftz(e.x), e.y > 0x1p126f ? 0.f : rcp_newton(e.y));  // 0 where rcp_ftz gives 0; NaN stays
 }
 
 // y = act(u) of two neighbouring channels; ib = 1 / (beta + 1e-9)

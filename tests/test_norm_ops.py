@@ -496,3 +496,24 @@ def test_silu_far_out(T, dtype):
         assert torch.all(got[..., 0] == float("inf")) and torch.isnan(got[..., odd[2:4]]).all()
         # -inf times a sigmoid of 0, or of 2^-126 where it is clamped there: never a finite number
         assert not torch.isfinite(got[..., odd[[1, 4]]]).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp16", "bf16"))
+@pytest.mark.parametrize("T", (40, 70000))
+def test_silu_far_out_in_both_channels_of_a_pair(T, dtype):
+    """Neighbouring channels that hold the same values give the same results, also where the exponential
+    overflows: 0 for finite arguments far below zero, NaN for -inf (0 times infinity), and no gradient."""
+    far = [-84.0, -86.0, -86.5, -87.0, -87.5, -88.0, -89.0, -100.0, -200.0, -1e4, -1e10, -1e30, -3e38, float("-inf"), float("inf"), float("nan")]
+    x = case(1, T, 16, "none", dtype, seed=3)[0].repeat_interleave(2, dim=2)
+    b = torch.tensor(far, device="cuda").repeat_interleave(2)
+    y, mean, rstd = pkg.group_norm_act(x, 4, None, b, act="silu")
+    dx, _, db, _, _ = pkg.group_norm_act_backward(torch.ones_like(x), x, mean, rstd, 4, None, b, act="silu")
+    even, odd = y[..., ::2].double(), y[..., 1::2].double()
+    assert torch.equal(torch.isnan(even), torch.isnan(odd))
+    # each is off by half a step of its type and a few units of 2^-24
+    near = (even - odd).abs() <= 1.01 * torch.finfo(x.dtype).eps * even.abs() + torch.finfo(x.dtype).smallest_normal
+    assert torch.all(near | torch.isnan(even) | (even == odd))
+    assert torch.all(y[..., 16:26] == 0) and torch.isnan(y[..., 26:28]).all() and torch.isnan(y[..., 30:]).all()
+    assert torch.all(y[..., 28:30] == float("inf"))
+    assert torch.all(db[16:26] == 0)
