@@ -852,9 +852,10 @@ mh3a_status check(const mh3a_norm* p) {
     if (p->act < MH3A_ACT_NONE || p->act > MH3A_ACT_SNAKE_BETA) return MH3A_ERR_INVALID_ARG;
     if (p->B < 1 || p->T < 1 || p->C < 1 || p->groups < 1 || p->C % p->groups) return MH3A_ERR_SHAPE;
     if (p->act == MH3A_ACT_SNAKE_BETA && (!p->alpha || !p->beta)) return MH3A_ERR_INVALID_ARG;
-    // row indices plus a block's stride stay in 32 bits; grids (at most one block per item and channel, or
-    // for 64 x 256 values) stay below 2^31
-    if (p->T > (1 << 30) || (long long)p->B * p->C >= (1LL << 31) || (long long)p->B * p->C * p->T >= (1LL << 40))
+    // In 32 bits stay: row indices plus a block's stride; channels and groups plus a tile's width or a block's
+    // threads, and the entries of a chunk (groups and channel tiles); grids, at most one block per item and channel, or
+    // for 64 x 256 values.
+    if (p->T > (1 << 30) || (long long)p->B * p->C >= (1LL << 30) || (long long)p->B * p->C * p->T >= (1LL << 40))
         return MH3A_ERR_SHAPE;
     return MH3A_OK;
 }

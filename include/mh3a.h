@@ -358,7 +358,7 @@ MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward, 
  * Errors: MH3A_ERR_INVALID_ARG (NULL p, x, y, mean or rstd; unknown dtype or act; alpha or beta
  * missing for SnakeBeta; a negative stride; a pointer not aligned to its element type;
  * a workspace missing, too small or misaligned), MH3A_ERR_SHAPE (B, T, C or groups below 1, groups
- * not dividing C, T above 2^30, B C of 2^31 or more, B T C of 2^40 or more), MH3A_ERR_CUDA. */
+ * not dividing C, T above 2^30, B C of 2^30 or more, B T C of 2^40 or more), MH3A_ERR_CUDA. */
 MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const void* x, long long x_batch_stride,
                                          long long x_row_stride, void* y, float* mean, float* rstd,
                                          void* workspace, size_t workspace_bytes, void* stream);

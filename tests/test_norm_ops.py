@@ -517,3 +517,19 @@ def test_silu_far_out_in_both_channels_of_a_pair(T, dtype):
     assert torch.all(y[..., 16:26] == 0) and torch.isnan(y[..., 26:28]).all() and torch.isnan(y[..., 30:]).all()
     assert torch.all(y[..., 28:30] == float("inf"))
     assert torch.all(db[16:26] == 0)
+
+
+def test_2_to_the_30_channels_are_refused():
+    """Channel indices plus a tile, and groups plus channel tiles, have to fit 32 bits: near 2^31 channels the
+    scratch size came out of a sum that had wrapped."""
+    L, ok = Bd.load(), 1 << 20
+    for B, Cn, groups in ((1, (1 << 31) - 1, (1 << 31) - 1), (1, 1 << 30, 1), (1 << 15, 1 << 15, 1 << 15), ((1 << 31) - 1, 1, 1)):
+        p = norm(dtype=0, B=B, T=1, C=Cn, groups=groups)
+        for backward in (0, 1):
+            assert L.mh3a_group_norm_act_workspace(C.byref(p), backward, 0) == 0
+        assert L.mh3a_group_norm_act(C.byref(p), ok, 0, 0, ok, ok, ok, ok, 1 << 40, None) == 3
+    # below: an entry of 16 bytes for every group and channel tile, or the sums of every channel and two means a group
+    most = (1 << 30) - 1
+    p = norm(dtype=0, B=1, T=1, C=most, groups=most)
+    assert L.mh3a_group_norm_act_workspace(C.byref(p), 0, 0) >= 16 * (most + most // 32)
+    assert L.mh3a_group_norm_act_workspace(C.byref(p), 1, 0) >= 4 * most * (2 + 2 + 2)
