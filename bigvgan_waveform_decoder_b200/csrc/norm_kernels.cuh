@@ -64,12 +64,6 @@ __device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
     return *reinterpret_cast<const Pack<T, V>*>(p);
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void unpack(const Pack<T, V>& p, float (&f)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = to_f<T>(p.v[i]);
-}
-
 // Pairs of neighbouring elements, for the packed fp32x2 instructions.
 __device__ __forceinline__ float2 pair_of(const float* v) { return make_float2(v[0], v[1]); }
 __device__ __forceinline__ float2 pair_of(const __half* v) { return __half22float2(*reinterpret_cast<const __half2*>(v)); }
@@ -99,27 +93,8 @@ __device__ __forceinline__ void store_pairs(T* p, const float2 (&f)[V / 2]) {
     *reinterpret_cast<Pack<T, V>*>(p) = o;
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void store_pack(T* p, const float (&f)[V]) {
-    Pack<T, V> o;
-    if constexpr (V % 2 == 0) {
-#pragma unroll
-        for (int i = 0; i < V; i += 2) put_pair(o.v + i, make_float2(f[i], f[i + 1]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) o.v[i] = from_f<T>(f[i]);
-    }
-    *reinterpret_cast<Pack<T, V>*>(p) = o;
-}
-
-// Loads V per-channel parameters; channels beyond C and a null array give `other`.
-template <int V>
-__device__ __forceinline__ void load_param(const float* p, int c, int C, float other, float (&f)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = (p && c + i < C) ? __ldg(p + c + i) : other;
-}
-
-// The same for a whole vector, by 16-byte loads: c is a multiple of V, C too, p 16-byte aligned.
+// V per-channel parameters by 16-byte loads, `other` for a null array: c is a multiple of V, C too, p 16-byte
+// aligned.
 template <int V>
 __device__ __forceinline__ void load_param_vec(const float* p, int c, float other, float2 (&f)[V / 2]) {
     if (p) {
