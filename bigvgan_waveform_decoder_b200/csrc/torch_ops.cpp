@@ -108,11 +108,14 @@ T* data(const Opt& t) { return t ? static_cast<T*>(t->data_ptr()) : nullptr; }
 
 // An output that a caller brings must not lie over an input: blocks would read what others have written.
 // (Views with gaps are trusted: whether two of them meet takes more to find out than a call takes.)
-void check_apart(const char* what, const Opt& out, const char* name, const Tensor& in) {
+void check_apart(const char* what, const Opt& out, std::initializer_list<std::pair<const char*, const Tensor*>> inputs) {
     if (!out) return;
-    const at::MemOverlapStatus st = at::get_overlap_status(*out, in);
-    if (st == at::MemOverlapStatus::Full || st == at::MemOverlapStatus::Partial)
-        refuse(what, MH3A_ERR_INVALID_ARG, "out overlaps ", name);
+    for (const auto& [name, in] : inputs) {
+        if (!in) continue;
+        const at::MemOverlapStatus st = at::get_overlap_status(*out, *in);
+        if (st == at::MemOverlapStatus::Full || st == at::MemOverlapStatus::Partial)
+            refuse(what, MH3A_ERR_INVALID_ARG, "out overlaps ", name);
+    }
 }
 
 void check_frames(const char* what, const char* name, const Tensor& x) {
@@ -163,7 +166,8 @@ std::tuple<Tensor, Tensor, Tensor> group_norm_act(const Tensor& x, int64_t group
     const mh3a_norm p = norm_args(what, x, groups, weight, bias, act, alpha, beta, eps, lengths);
     const c10::Device device = x.device();
     if (out) check_plain(what, "out", *out, device, x.scalar_type(), x.sizes());
-    check_apart(what, out, "x", x);
+    check_apart(what, out, {{"x", &x}, {"weight", opt(weight)}, {"bias", opt(bias)}, {"alpha", opt(alpha)}, {"beta", opt(beta)},
+                            {"lengths", opt(lengths)}});
     const Launch on(device, stream);
     Tensor y = out ? *out : empty(x.sizes(), x.scalar_type(), device);
     Tensor mean = empty({p.B, groups}, at::kFloat, device), rstd = empty({p.B, groups}, at::kFloat, device);
@@ -301,8 +305,7 @@ Tensor fp8_matmul(const Tensor& a, const Tensor& a_scale, const Tensor& b, const
     require(a.device() == b.device(), what, "a and b are on different devices");
     if (dtype_of(out_dtype) < 0) refuse(what, MH3A_ERR_INVALID_ARG, "out_dtype is ", out_dtype);
     check_bias_out(what, bias, out, a.device(), sa.rows, sb.rows, out_dtype);
-    check_apart(what, out, "a", a);
-    check_apart(what, out, "b", b);
+    check_apart(what, out, {{"a", &a}, {"b", &b}, {"a_scale", &a_scale}, {"b_scale", &b_scale}, {"bias", opt(bias)}});
     const Launch on(a.device(), stream);
     const Tensor y = out ? *out : empty({sa.rows, sb.rows}, out_dtype, a.device());
     check(mh3a_fp8_matmul(a.data_ptr(), sa.stride, a_scale.data_ptr<float>(), b.data_ptr(), sb.stride, b_scale.data_ptr<float>(),
@@ -323,8 +326,7 @@ Tensor fp8_linear(const Tensor& x, const Tensor& w, const Tensor& w_scale, const
     if (K != sw.cols) refuse(what, MH3A_ERR_SHAPE, "x has ", K, " columns and w ", sw.cols);
     require(x.device() == w.device(), what, "x and w are on different devices");
     check_bias_out(what, bias, out, x.device(), M, N, x.scalar_type());
-    check_apart(what, out, "x", x);
-    check_apart(what, out, "w", w);
+    check_apart(what, out, {{"x", &x}, {"w", &w}, {"w_scale", &w_scale}, {"bias", opt(bias)}});
     const Launch on(x.device(), stream);
     const Tensor y = out ? *out : empty({M, N}, x.scalar_type(), x.device());
     const size_t n = mh3a_fp8_linear_workspace((int)M, (int)N, (int)K);

@@ -38,7 +38,7 @@ def group_norm_act(x, groups, weight=None, bias=None, act="none", alpha=None, be
     C.  weight, bias: float32 [C] or None.  act: "none", "silu" or "snake_beta", the last with float32
     alpha and beta [C].  lengths: int32 [B], the valid rows of each item; rows behind them are not read
     and are zeros in y.  Returns (y, mean, rstd): y like x and contiguous (``out`` if given, which must
-    not overlap x), mean and rstd float32 [B, groups], which group_norm_act_backward takes."""
+    not overlap an input), mean and rstd float32 [B, groups], which group_norm_act_backward takes."""
     return _ops.group_norm_act(x, groups, weight, bias, act, alpha, beta, eps, lengths, out, _stream(stream))
 
 
@@ -64,7 +64,7 @@ def fp8_quantize(x, block_rows=1, transpose=False, stream=None):
 def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, bias=None, out=None, stream=None):
     """a [M, K] times b [N, K] transposed, plus bias [N] (float32), for fp8 matrices as fp8_quantize returns
     them: a with block_rows 1, b with 1 or 128 (mh3a_fp8_matmul).  Sums are fp32, rounded once to
-    ``out_dtype``.  Returns [M, N] (``out`` if given, which must not overlap an operand)."""
+    ``out_dtype``.  Returns [M, N] (``out`` if given, which must not overlap an input)."""
     return _ops.fp8_matmul(a, a_scale, b, b_scale, out_dtype, bias, out, _stream(stream))
 
 
@@ -72,5 +72,5 @@ def fp8_linear(x, w, w_scale, bias=None, out=None, stream=None):
     """x [M, K] times w [N, K] transposed, plus bias: x (float32, float16 or bfloat16) is quantised with
     block_rows 1, w and w_scale come from fp8_quantize (mh3a_fp8_linear).  For channels-last frames
     [B, T, C] pass x.view(B * T, C).  Returns [M, N] of x's type (``out`` if given, which must not overlap
-    x or w)."""
+    an input)."""
     return _ops.fp8_linear(x, w, w_scale, bias, out, _stream(stream))

@@ -351,7 +351,7 @@ MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward, 
  *   u = (x - mean) rstd weight_c + bias_c,   y = act(u).
  * x: device, channels adjacent, item b and row t at x + b x_batch_stride + t x_row_stride
  * elements (strides >= 0; 0 repeats an item or a row).  y: device [B, T, C], contiguous, must not
- * overlap x.  mean, rstd: device [B, groups], what the backward pass needs.  An item of no valid
+ * overlap an input.  mean, rstd: device [B, groups], what the backward pass needs.  An item of no valid
  * rows has mean 0 and var 0.  All arithmetic is fp32 (combining partial statistics: fp64), rounded once to the type of y.
  * `workspace`: device, 16-byte aligned, at least mh3a_group_norm_act_workspace(p, 0, aligned) bytes
  * (NULL where that is 0).
@@ -364,7 +364,7 @@ MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const void* x, long
                                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients of mh3a_group_norm_act at x for the output gradient dy (strides as for x); mean and
- * rstd are the forward pass's.  dx: device [B, T, C], contiguous, must not overlap x or dy.
+ * rstd are the forward pass's.  dx: device [B, T, C], contiguous, must not overlap an input.
  * dweight, dbias, dalpha, dbeta: device [C] fp32, summed over all items and valid rows; each may
  * be NULL when it is not wanted (dalpha and dbeta must be NULL unless act is
  * MH3A_ACT_SNAKE_BETA).  Errors as mh3a_group_norm_act. */
@@ -400,7 +400,7 @@ MH3A_API mh3a_status mh3a_fp8_quantize(const void* x, int dtype, int rows, int c
  * b_block_rows 1 or 128, both as above.  The products of a block are added on the tensor cores, the
  * blocks scaled and added in fp32; the sum is rounded once to out_dtype (mh3a_dtype).  bias: device
  * fp32 [N] or NULL.  out: device, columns adjacent, rows out_stride elements apart; must not overlap
- * an operand.  Errors: MH3A_ERR_INVALID_ARG (NULL or misaligned pointers, unknown dtype,
+ * an input.  Errors: MH3A_ERR_INVALID_ARG (NULL or misaligned pointers, unknown dtype,
  * b_block_rows other than 1 or 128, a stride below the row's length, an operand's stride not a
  * multiple of 16 or 2^40 or more), MH3A_ERR_SHAPE (M, N or K below 1 or above 2^30, or more than
  * 2^30 output tiles), MH3A_ERR_CUDA. */
@@ -413,7 +413,7 @@ MH3A_API mh3a_status mh3a_fp8_matmul(const void* a, long long a_stride, const fl
  * mh3a_fp8_matmul with y of the same dtype.  One to MH3A_FP8_FEW_ROWS rows of a layer that is not
  * large run as one kernel that is bound by reading the weights, for a decode frame by frame.
  * `workspace`: device, 16-byte aligned, mh3a_fp8_linear_workspace(M, N, K) bytes (0 for that kernel;
- * it may be NULL then).  y must not overlap x or w.  Errors: as the two calls, and MH3A_ERR_INVALID_ARG for a workspace too small
+ * it may be NULL then).  y must not overlap an input.  Errors: as the two calls, and MH3A_ERR_INVALID_ARG for a workspace too small
  * or misaligned. */
 #define MH3A_FP8_FEW_ROWS 4
 MH3A_API size_t mh3a_fp8_linear_workspace(int M, int N, int K);

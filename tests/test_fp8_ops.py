@@ -433,3 +433,34 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(pkg.fp8_matmul(w, sw, far, sf), pkg.fp8_matmul(w, sw, w[:3], sf))
     assert torch.equal(pkg.fp8_matmul(far, sf, w, sw), pkg.fp8_matmul(w[:3], sf, w, sw))
     assert torch.equal(pkg.fp8_linear(x[:2], far, sf), pkg.fp8_linear(x[:2], w[:3], sf))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ("w_scale", "bias", "a_scale"))
+def test_an_output_over_scales_or_bias_is_refused(name):
+    M, N, K = 20, 256, 256
+    x = rand(M, K)
+    w, sw = pkg.fp8_quantize(rand(N, K, seed=1), block_rows=128)
+    q, s = pkg.fp8_quantize(x)
+    bias = rand(N, seed=2)
+    buf = torch.zeros(M * N + 2 * N, device="cuda")
+    out = buf[N:-N].view(M, N)
+
+    def calls(at):
+        like = dict(w_scale=sw, bias=bias, a_scale=s)[name]
+        part = buf[N + at:][:like.numel()].view(like.shape)
+        part.copy_(like)
+        kw = {"w_scale": sw, "bias": bias, "a_scale": s, name: part}
+        if name != "a_scale":
+            yield lambda: pkg.fp8_linear(x, w, kw["w_scale"], kw["bias"], out=out)
+        yield lambda: pkg.fp8_matmul(q, kw["a_scale"], w, kw["w_scale"], torch.float32, bias=kw["bias"], out=out)
+
+    names = dict(w_scale="(w|b)_scale", bias="bias", a_scale="a_scale")
+    for at in (0, 1000, M * N - 1):
+        for call in calls(at):
+            with pytest.raises(pkg.MH3AError, match="out overlaps " + names[name]) as e:
+                call()
+            assert e.value.status == 1
+    want = pkg.fp8_linear(x, w, sw, bias)
+    for call in calls(M * N):  # side by side
+        assert torch.equal(call(), want)

@@ -533,3 +533,23 @@ def test_2_to_the_30_channels_are_refused():
     p = norm(dtype=0, B=1, T=1, C=most, groups=most)
     assert L.mh3a_group_norm_act_workspace(C.byref(p), 0, 0) >= 16 * (most + most // 32)
     assert L.mh3a_group_norm_act_workspace(C.byref(p), 1, 0) >= 4 * most * (2 + 2 + 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ("weight", "bias", "alpha", "beta", "lengths"))
+def test_an_output_over_a_parameter_is_refused(name):
+    B, T, Cn = 2, 3, 16
+    x, w, b, al, be = case(B, T, Cn, "snake_beta", "fp32", seed=1)
+    buf = torch.ones(B * T * Cn + 2 * Cn, device="cuda")
+    kw = dict(weight=w, bias=b, alpha=al, beta=be, lengths=None)
+    size = B if name == "lengths" else Cn
+    for at in (0, 7, B * T * Cn - 1):  # the first, one inside, across the end
+        part = buf[Cn:][at:at + size]
+        kw[name] = part.view(torch.int32) if name == "lengths" else part
+        with pytest.raises(pkg.MH3AError, match="out overlaps " + name) as e:
+            pkg.group_norm_act(x, 4, act="snake_beta", out=buf[Cn:-Cn].view(B, T, Cn), **kw)
+        assert e.value.status == 1
+    for at in (Cn - size, Cn + B * T * Cn):  # side by side
+        part = buf[at:at + size]
+        kw[name] = part.view(torch.int32) if name == "lengths" else part
+        pkg.group_norm_act(x, 4, act="snake_beta", out=buf[Cn:-Cn].view(B, T, Cn), **kw)
