@@ -2,11 +2,12 @@
 // allocation around the C ABI of include/mh3a.h, nothing else.  It is compiled code because the
 // smallest calls take 3 to 4 us on the GPU: the same marshalling in Python took 19 us a call.
 #include <ATen/ATen.h>
-#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/extension.h>
+
+#include <algorithm>
 
 #include "mh3a.h"
 
@@ -106,16 +107,68 @@ bool aligned16(const Opt& t) { return !t || aligned16(*t); }
 template <typename T>
 T* data(const Opt& t) { return t ? static_cast<T*>(t->data_ptr()) : nullptr; }
 
+// The bytes of a tensor whose last dimension is adjacent: `items` x `rows` runs of `run` bytes from `at` on.
+struct Bytes {
+    int64_t at, run, row, rows, item, items;
+
+    explicit Bytes(const Tensor& t) {
+        const int64_t e = t.element_size(), d = t.dim();
+        at = reinterpret_cast<intptr_t>(t.data_ptr());
+        run = t.size(d - 1) * e;
+        rows = d > 1 ? t.size(d - 2) : 1;
+        row = d > 1 ? stride_of(t, d - 2) * e : 0;
+        items = d > 2 ? t.size(d - 3) : 1;
+        item = d > 2 ? stride_of(t, d - 3) * e : 0;
+        if (rows == 1) {  // the items are the rows
+            rows = items;
+            row = item;
+            items = 1;
+            item = 0;
+        } else if (items > 1 && item == rows * row) {  // one follows the other as the rows do
+            rows *= items;
+            items = 1;
+            item = 0;
+        }
+        if (rows > 1 && row == run) {
+            run *= rows;
+            rows = 1;
+            row = 0;
+        }
+    }
+    int64_t end() const { return at + (items - 1) * item + (rows - 1) * row + run; }
+};
+
+// Whether some run of `n` of them, `step` apart (>= 0) from `at` on, meets [from, to).
+bool runs_meet(int64_t at, int64_t run, int64_t step, int64_t n, int64_t from, int64_t to) {
+    if (step == 0) return at < to && at + run > from;
+    const int64_t first = from - run - at < 0 ? 0 : (from - run - at) / step + 1;  // ends behind `from`
+    return first < n && at + first * step < to;
+}
+
+bool meet(const Bytes& a, const Bytes& b) {
+    if (a.at >= b.end() || b.at >= a.end()) return false;
+    if (a.items == 1 && b.items == 1 && a.row == b.row && a.row >= std::max(a.run, b.run)) {
+        // rows as far apart, as columns of one buffer have them: row i of a begins `r` bytes into the place of row i + q of b
+        const int64_t d = a.at - b.at, q = d >= 0 ? d / a.row : -((-d + a.row - 1) / a.row), r = d - q * a.row;
+        auto row_there = [&](int64_t k) { return k < b.rows && k + a.rows > 0; };  // some i with 0 <= i + k < b.rows
+        return (r < b.run && row_there(q)) || (r + a.run > a.row && row_there(q + 1));
+    }
+    const Bytes &few = a.rows * a.items <= b.rows * b.items ? a : b, &many = &few == &a ? b : a;
+    for (int64_t i = 0; i < few.items; ++i)
+        for (int64_t r = 0; r < few.rows; ++r) {
+            const int64_t from = few.at + i * few.item + r * few.row;
+            for (int64_t k = 0; k < many.items; ++k)
+                if (runs_meet(many.at + k * many.item, many.run, many.row, many.rows, from, from + few.run)) return true;
+        }
+    return false;
+}
+
 // An output that a caller brings must not lie over an input: blocks would read what others have written.
-// (Views with gaps are trusted: whether two of them meet takes more to find out than a call takes.)
 void check_apart(const char* what, const Opt& out, std::initializer_list<std::pair<const char*, const Tensor*>> inputs) {
     if (!out) return;
-    for (const auto& [name, in] : inputs) {
-        if (!in) continue;
-        const at::MemOverlapStatus st = at::get_overlap_status(*out, *in);
-        if (st == at::MemOverlapStatus::Full || st == at::MemOverlapStatus::Partial)
-            refuse(what, MH3A_ERR_INVALID_ARG, "out overlaps ", name);
-    }
+    const Bytes to(*out);
+    for (const auto& [name, in] : inputs)
+        if (in && meet(to, Bytes(*in))) refuse(what, MH3A_ERR_INVALID_ARG, "out overlaps ", name);
 }
 
 void check_frames(const char* what, const char* name, const Tensor& x) {

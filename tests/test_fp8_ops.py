@@ -1,5 +1,6 @@
 """fp8 matrices with one scale for each block of 128 values: quantisation, product, linear layer."""
 import ctypes as C
+import random
 
 import pytest
 import torch
@@ -8,6 +9,7 @@ import bigvgan_waveform_decoder_b200 as pkg
 from bigvgan_waveform_decoder_b200 import binding as Bd
 
 from . import ops_ref as R
+from .test_norm_ops import places
 
 TYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
 
@@ -464,3 +466,27 @@ def test_an_output_over_scales_or_bias_is_refused(name):
     want = pkg.fp8_linear(x, w, sw, bias)
     for call in calls(M * N):  # side by side
         assert torch.equal(call(), want)
+
+
+@pytest.mark.gpu
+def test_views_of_one_buffer_are_refused_where_they_meet():
+    """Random rows with gaps of one buffer as input and output: refused if, and only if, they share an element."""
+    rng = random.Random(6)
+    buf = torch.randn(6000, device="cuda")
+    met = 0
+    for _ in range(400):
+        M, N, K = rng.choice([(1, 8, 24), (6, 8, 8), (5, 16, 24), (9, 24, 8)])
+        w, sw = pkg.fp8_quantize(rand(N, K, seed=K), block_rows=128)
+        xs = rng.choice([0, 5, K, K + N, 64, 96])
+        os = rng.choice([N, N + 3, K + N, xs if xs >= N else 64, 96])
+        x = buf.as_strided((M, K), (xs, 1), rng.randrange(1200))
+        out = buf.as_strided((M, N), (os, 1), rng.randrange(1200))
+        if places(x) & places(out):
+            met += 1
+            with pytest.raises(pkg.MH3AError, match="out overlaps x"):
+                pkg.fp8_linear(x, w, sw, out=out)
+        else:
+            want = pkg.fp8_linear(x, w, sw)
+            assert torch.equal(pkg.fp8_linear(x, w, sw, out=out), want)
+            buf.normal_()
+    assert met > 40

@@ -1,5 +1,6 @@
 """Group norm with an activation over channels-last frames, against its formulas in 64 bits."""
 import ctypes as C
+import random
 import time
 
 import pytest
@@ -553,3 +554,40 @@ def test_an_output_over_a_parameter_is_refused(name):
         part = buf[at:at + size]
         kw[name] = part.view(torch.int32) if name == "lengths" else part
         pkg.group_norm_act(x, 4, act="snake_beta", out=buf[Cn:-Cn].view(B, T, Cn), **kw)
+
+
+def places(t):
+    """The places of a view's elements in its storage."""
+    at = torch.tensor(t.storage_offset())
+    for n, s in zip(t.shape, t.stride()):
+        at = at[..., None] + torch.arange(n) * s
+    return set(at.flatten().tolist())
+
+
+@pytest.mark.gpu
+def test_views_of_one_buffer_are_refused_where_they_meet():
+    """Random views with gaps, repeated and overlapping rows: refused if, and only if, they share an element."""
+    rng = random.Random(5)
+    buf = torch.randn(7000, device="cuda")
+    met = 0
+    for _ in range(400):
+        B, T, Cn = rng.choice([(1, 5, 8), (3, 4, 8), (2, 1, 16), (4, 7, 4)])
+        row = rng.choice([0, 3, Cn, Cn + 4, 5 * Cn, 96])
+        item = rng.choice([0, Cn, row * T, row * T + 8, 2 * row * T + 1])
+        out = buf[(at := rng.randrange(1500)):at + B * T * Cn].view(B, T, Cn)
+        x = buf.as_strided((B, T, Cn), (item, row, 1), rng.randrange(1500))
+        if places(x) & places(out):
+            met += 1
+            with pytest.raises(pkg.MH3AError, match="out overlaps x"):
+                pkg.group_norm_act(x, 2, out=out)
+        else:
+            # (the way a call goes depends on the output's alignment, so bits may differ from a call without `out`)
+            check_forward(x, 2, None, None, "none", None, None, got=pkg.group_norm_act(x, 2, out=out))
+            buf.normal_()
+    assert met > 40
+    # the same view twice, and its neighbour's columns
+    wide = torch.randn(2, 30, 64, device="cuda")
+    some = wide[:1, :, :32]
+    with pytest.raises(pkg.MH3AError, match="out overlaps x"):
+        pkg.group_norm_act(wide[1:, ::2, 8:40], 2, out=wide.view(-1)[40 * 64:][:15 * 32].view(1, 15, 32))
+    assert some.shape == pkg.group_norm_act(some, 2, out=wide.view(-1)[30 * 64:][:30 * 32].view(1, 30, 32))[0].shape
