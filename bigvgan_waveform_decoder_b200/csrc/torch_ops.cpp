@@ -5,6 +5,8 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/extension.h>
 
 #include <algorithm>
@@ -69,6 +71,31 @@ class Launch {
 };
 
 const Tensor* opt(const Opt& t) { return t ? &*t : nullptr; }
+
+// The calls record no gradient.  Where autograd is recording and an input requires one, the results lead
+// back to a node that raises, so that none is lost without a word; as for torch's own operators, `out` is
+// refused then.
+class NoGradient {
+  public:
+    NoGradient(const char* what, const char* instead, const Tensor* out, std::initializer_list<const Tensor*> inputs) {
+        if (!at::GradMode::is_enabled()) return;
+        torch::autograd::edge_list edges;
+        for (const Tensor* t : inputs)
+            if (t && t->requires_grad()) edges.push_back(torch::autograd::impl::gradient_edge(*t));
+        if (edges.empty() && !(out && out->requires_grad())) return;
+        if (out) refuse(what, MH3A_ERR_INVALID_ARG, "out cannot be given where an input or out requires a gradient");
+        node_ = std::shared_ptr<torch::autograd::Node>(
+            new torch::autograd::Error(c10::str(what, " records no gradient: ", instead, ", or detach its inputs"), std::move(edges)),
+            torch::autograd::deleteNode);
+    }
+    void from(std::initializer_list<const Tensor*> results) const {
+        if (node_)
+            for (const Tensor* t : results) torch::autograd::set_history(*t, node_);
+    }
+
+  private:
+    std::shared_ptr<torch::autograd::Node> node_;
+};
 
 int dtype_of(at::ScalarType t) {
     switch (t) {
@@ -221,6 +248,7 @@ std::tuple<Tensor, Tensor, Tensor> group_norm_act(const Tensor& x, int64_t group
     if (out) check_plain(what, "out", *out, device, x.scalar_type(), x.sizes());
     check_apart(what, out, {{"x", &x}, {"weight", opt(weight)}, {"bias", opt(bias)}, {"alpha", opt(alpha)}, {"beta", opt(beta)},
                             {"lengths", opt(lengths)}});
+    const NoGradient none(what, "call group_norm_act_backward", opt(out), {&x, opt(weight), opt(bias), opt(alpha), opt(beta)});
     const Launch on(device, stream);
     Tensor y = out ? *out : empty(x.sizes(), x.scalar_type(), device);
     Tensor mean = empty({p.B, groups}, at::kFloat, device), rstd = empty({p.B, groups}, at::kFloat, device);
@@ -233,6 +261,7 @@ std::tuple<Tensor, Tensor, Tensor> group_norm_act(const Tensor& x, int64_t group
           what);
     on.inputs({&x, opt(weight), opt(bias), opt(alpha), opt(beta), opt(lengths), opt(out)});
     on.outputs({&y, &mean, &rstd});
+    none.from({&y, &mean, &rstd});
     return {y, mean, rstd};
 }
 
@@ -250,6 +279,8 @@ std::tuple<Tensor, Opt, Opt, Opt, Opt> group_norm_act_backward(const Tensor& dy,
     const int64_t stats[2] = {p.B, groups};
     check_plain(what, "mean", mean, device, at::kFloat, stats);
     check_plain(what, "rstd", rstd, device, at::kFloat, stats);
+    const NoGradient none(what, "it is a gradient itself", nullptr,
+                          {&dy, &x, &mean, &rstd, opt(weight), opt(bias), opt(alpha), opt(beta)});
     const Launch on(device, stream);
     const Tensor dx = empty(x.sizes(), x.scalar_type(), device);
     const Opt* params[4] = {&weight, &bias, &alpha, &beta};
@@ -267,8 +298,12 @@ std::tuple<Tensor, Opt, Opt, Opt, Opt> group_norm_act_backward(const Tensor& dy,
           what);
     on.inputs({&dy, &x, &mean, &rstd, opt(weight), opt(bias), opt(alpha), opt(beta), opt(lengths)});
     on.outputs({&dx});
+    none.from({&dx});
     for (const Opt& g : grads)
-        if (g) on.outputs({&*g});
+        if (g) {
+            on.outputs({&*g});
+            none.from({&*g});
+        }
     return {dx, grads[0], grads[1], grads[2], grads[3]};
 }
 
@@ -336,6 +371,7 @@ std::tuple<Tensor, Tensor> fp8_quantize(const Tensor& x, int64_t block_rows, boo
     check_values(what, "x", x);
     if (block_rows != 1 && block_rows != kBlock) refuse(what, MH3A_ERR_INVALID_ARG, "block_rows is ", block_rows, ": 1 or 128 is wanted");
     const int64_t rows = x.size(0), cols = x.size(1), outer = transpose ? cols : rows, inner = transpose ? rows : cols;
+    const NoGradient none(what, "differentiate what it is used for", nullptr, {&x});
     const Launch on(x.device(), stream);
     const int64_t ld = (inner + 15) / 16 * 16;
     Tensor q = empty({outer, ld}, at::kFloat8_e4m3fn, x.device());
@@ -345,6 +381,7 @@ std::tuple<Tensor, Tensor> fp8_quantize(const Tensor& x, int64_t block_rows, boo
           what);
     on.inputs({&x});
     on.outputs({&q, &scale});
+    none.from({&q, &scale});
     if (ld != inner) q = q.narrow(1, 0, inner);
     return {q, scale};
 }
@@ -359,6 +396,7 @@ Tensor fp8_matmul(const Tensor& a, const Tensor& a_scale, const Tensor& b, const
     if (dtype_of(out_dtype) < 0) refuse(what, MH3A_ERR_INVALID_ARG, "out_dtype is ", out_dtype);
     check_bias_out(what, bias, out, a.device(), sa.rows, sb.rows, out_dtype);
     check_apart(what, out, {{"a", &a}, {"b", &b}, {"a_scale", &a_scale}, {"b_scale", &b_scale}, {"bias", opt(bias)}});
+    const NoGradient none(what, "form the products of the gradients", opt(out), {&a, &a_scale, &b, &b_scale, opt(bias)});
     const Launch on(a.device(), stream);
     const Tensor y = out ? *out : empty({sa.rows, sb.rows}, out_dtype, a.device());
     check(mh3a_fp8_matmul(a.data_ptr(), sa.stride, a_scale.data_ptr<float>(), b.data_ptr(), sb.stride, b_scale.data_ptr<float>(),
@@ -367,6 +405,7 @@ Tensor fp8_matmul(const Tensor& a, const Tensor& a_scale, const Tensor& b, const
           what);
     on.inputs({&a, &a_scale, &b, &b_scale, opt(bias), opt(out)});
     on.outputs({&y});
+    none.from({&y});
     return y;
 }
 
@@ -380,6 +419,7 @@ Tensor fp8_linear(const Tensor& x, const Tensor& w, const Tensor& w_scale, const
     require(x.device() == w.device(), what, "x and w are on different devices");
     check_bias_out(what, bias, out, x.device(), M, N, x.scalar_type());
     check_apart(what, out, {{"x", &x}, {"w", &w}, {"w_scale", &w_scale}, {"bias", opt(bias)}});
+    const NoGradient none(what, "call fp8_linear and fp8_matmul on the transposed operands", opt(out), {&x, &w, &w_scale, opt(bias)});
     const Launch on(x.device(), stream);
     const Tensor y = out ? *out : empty({M, N}, x.scalar_type(), x.device());
     const size_t n = mh3a_fp8_linear_workspace((int)M, (int)N, (int)K);
@@ -391,6 +431,7 @@ Tensor fp8_linear(const Tensor& x, const Tensor& w, const Tensor& w_scale, const
           what);
     on.inputs({&x, &w, &w_scale, opt(bias), opt(out)});
     on.outputs({&y});
+    none.from({&y});
     return y;
 }
 

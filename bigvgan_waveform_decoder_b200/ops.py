@@ -10,7 +10,9 @@ results and the scratch memory.  Tensors are CUDA tensors of one device; a call 
 scratch are allocated on that stream; ordering the caller's own tensors with it stays the caller's
 business, as everywhere in CUDA, but tensors that are still in use there are kept from the allocator
 until the call is done.  Bad arguments raise ``MH3AError`` before anything is launched.  The calls
-record no autograd graph: a gradient is a call of its own.
+record no gradient: it is a call of its own, for a ``torch.autograd.Function`` to make.  Where autograd is
+recording and an input requires a gradient, the results lead back to a node that raises when a backward pass
+reaches it, and ``out`` is refused; under ``torch.no_grad()`` or with detached inputs nothing is recorded.
 """
 from __future__ import annotations
 

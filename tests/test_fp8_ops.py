@@ -490,3 +490,31 @@ def test_views_of_one_buffer_are_refused_where_they_meet():
             assert torch.equal(pkg.fp8_linear(x, w, sw, out=out), want)
             buf.normal_()
     assert met > 40
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", (128, 40))
+def test_gradients_are_not_lost_without_a_word(K):
+    """Where autograd is recording, results lead back to a node that raises; elsewhere they are plain."""
+    x, bias = rand(6, K), rand(32, seed=3)
+    w, sw = pkg.fp8_quantize(rand(32, K, seed=1), block_rows=128)
+    q, s = pkg.fp8_quantize(x)
+    assert not any(t.requires_grad for t in (w, sw, q, s, pkg.fp8_linear(x, w, sw, bias)))
+
+    def req(t):
+        return t.clone().requires_grad_()
+
+    for call, used in ((lambda: pkg.fp8_linear(req(x), w, sw), "fp8_linear"), (lambda: pkg.fp8_linear(x, w, req(sw)), "fp8_linear"),
+                       (lambda: pkg.fp8_linear(x, w, sw, req(bias)), "fp8_linear"),
+                       (lambda: pkg.fp8_matmul(q, req(s), w, sw), "fp8_matmul"),
+                       (lambda: pkg.fp8_matmul(q, s, w, sw, bias=req(bias)), "fp8_matmul"),
+                       (lambda: pkg.fp8_quantize(req(x))[0], "fp8_quantize"), (lambda: pkg.fp8_quantize(req(x))[1], "fp8_quantize"),
+                       (lambda: pkg.fp8_linear(x, *pkg.fp8_quantize(req(rand(32, K)), block_rows=128)), "fp8_linear")):
+        with pytest.raises(RuntimeError, match=f"mh3a_{used} records no gradient"):
+            call().float().sum().backward()
+        with torch.no_grad():
+            assert not call().requires_grad
+    out = torch.empty(6, 32, device="cuda")
+    with pytest.raises(pkg.MH3AError, match="out cannot be given"):
+        pkg.fp8_linear(req(x), w, sw, out=out)
+    assert torch.equal(pkg.fp8_linear(x, w, sw, out=out), pkg.fp8_linear(x, w, sw))

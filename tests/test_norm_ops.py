@@ -591,3 +591,56 @@ def test_views_of_one_buffer_are_refused_where_they_meet():
     with pytest.raises(pkg.MH3AError, match="out overlaps x"):
         pkg.group_norm_act(wide[1:, ::2, 8:40], 2, out=wide.view(-1)[40 * 64:][:15 * 32].view(1, 15, 32))
     assert some.shape == pkg.group_norm_act(some, 2, out=wide.view(-1)[30 * 64:][:30 * 32].view(1, 30, 32))[0].shape
+
+
+@pytest.mark.gpu
+def test_gradients_are_not_lost_without_a_word():
+    """Where autograd is recording, results lead back to a node that raises; elsewhere they are plain."""
+    x, w, b, al, be = case(2, 5, 16, "snake_beta", "fp32", seed=2)
+    args = dict(x=x, weight=w, bias=b, alpha=al, beta=be)
+    for name in args:
+        kw = {**args, name: args[name].clone().requires_grad_()}
+        for k in range(3):
+            r = pkg.group_norm_act(kw["x"], 4, kw["weight"], kw["bias"], act="snake_beta", alpha=kw["alpha"], beta=kw["beta"])[k]
+            with pytest.raises(RuntimeError, match="mh3a_group_norm_act records no gradient: call group_norm_act_backward"):
+                (3 * r).sum().backward()
+            assert kw[name].grad is None
+        with pytest.raises(pkg.MH3AError, match="out cannot be given"):
+            pkg.group_norm_act(kw["x"], 4, kw["weight"], kw["bias"], act="snake_beta", alpha=kw["alpha"], beta=kw["beta"],
+                               out=torch.empty_like(x))
+        with torch.no_grad():
+            got = pkg.group_norm_act(kw["x"], 4, kw["weight"], kw["bias"], act="snake_beta", alpha=kw["alpha"], beta=kw["beta"],
+                                     out=torch.empty_like(x))
+            assert not any(t.requires_grad for t in got)
+    with pytest.raises(pkg.MH3AError, match="out cannot be given"):
+        pkg.group_norm_act(x, 4, out=torch.empty_like(x).requires_grad_())
+    y, m, r = pkg.group_norm_act(x, 4, w, b)
+    assert not (y.requires_grad or m.requires_grad or r.requires_grad)
+    for dx in pkg.group_norm_act_backward(y.clone().requires_grad_(), x, m, r, 4, w, b)[:3]:
+        with pytest.raises(RuntimeError, match="records no gradient"):
+            dx.sum().backward()
+
+
+class NormAct(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, al, be):
+        y, mean, rstd = pkg.group_norm_act(x, 4, w, b, act="snake_beta", alpha=al, beta=be)
+        ctx.save_for_backward(x, mean, rstd, w, b, al, be)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, mean, rstd, w, b, al, be = ctx.saved_tensors
+        return pkg.group_norm_act_backward(dy, x, mean, rstd, 4, w, b, act="snake_beta", alpha=al, beta=be)
+
+
+@pytest.mark.gpu
+def test_inside_an_autograd_function():
+    x, w, b, al, be = case(2, 50, 16, "snake_beta", "fp32", seed=3)
+    dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(1)).cuda()
+    leaves = [t.clone().requires_grad_() for t in (x, w, b, al, be)]
+    y = NormAct.apply(*leaves)
+    y.backward(dy)
+    plain, mean, rstd = pkg.group_norm_act(x, 4, w, b, act="snake_beta", alpha=al, beta=be)
+    want = pkg.group_norm_act_backward(dy, x, mean, rstd, 4, w, b, act="snake_beta", alpha=al, beta=be)
+    assert torch.equal(y, plain) and all(torch.equal(t.grad, g) for t, g in zip(leaves, want))
