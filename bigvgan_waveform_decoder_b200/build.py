@@ -3,12 +3,13 @@
     python -m bigvgan_waveform_decoder_b200.build     # writes bigvgan_waveform_decoder_b200/libmh3a.so
 
 nvcc compiles every csrc/*.cu for sm_100a and links one shared library exporting the C ABI of
-include/mh3a.h.  It then builds _ops.so, the operators' front end for torch tensors, on that library
-and the installed torch.  No GPU is needed to build.
+include/mh3a.h.  Where torch is installed it then builds _ops.so, the operators' front end for torch
+tensors, on that library and that torch.  No GPU is needed to build.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -50,8 +51,12 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
+    """Both; without torch the library alone, which is all that the decoder needs."""
     build_library(force, verbose, extra)
-    build_ops(force, verbose)
+    if importlib.util.find_spec("torch") is None:
+        print("torch is not installed: the operators' front end (_ops.so) is not built", file=sys.stderr)
+    else:
+        build_ops(force, verbose)
     return LIB
 
 
