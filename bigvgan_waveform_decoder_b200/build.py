@@ -13,6 +13,8 @@ import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
+from importlib import metadata
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmh3a.so")
 OPS_SRC = os.path.join(CSRC, "torch_ops.cpp")
 OPS = os.path.join(HERE, "_ops.so")
+OPS_STAMP = os.path.join(HERE, "_build", "_ops.stamp")  # what OPS was built for
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -60,13 +63,25 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     return LIB
 
 
+def ops_stamp() -> str:
+    """What else than its sources _ops.so depends on: torch, Python and the compiler."""
+    return "\n".join((metadata.version("torch"), sysconfig.get_config_var("SOABI"), NVCC))
+
+
+def _ops_stamp_is(stamp) -> bool:
+    try:
+        with open(OPS_STAMP) as f:
+            return f.read() == stamp
+    except OSError:
+        return False
+
+
 def build_ops(force: bool = False, verbose: bool = False) -> str:
     """_ops.so: csrc/torch_ops.cpp against libmh3a.so and torch."""
     header = os.path.join(ROOT, "include", "mh3a.h")
-    if not force and _newer(OPS, [OPS_SRC, header, os.path.abspath(__file__)]):
+    stamp = ops_stamp()
+    if not force and _ops_stamp_is(stamp) and _newer(OPS, [OPS_SRC, header, os.path.abspath(__file__)]):
         return OPS
-    import sysconfig
-
     import torch
     from torch.utils.cpp_extension import include_paths
 
@@ -84,6 +99,9 @@ def build_ops(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, OPS)
+    os.makedirs(os.path.dirname(OPS_STAMP), exist_ok=True)
+    with open(OPS_STAMP, "w") as f:
+        f.write(stamp)
     return OPS
 
 

@@ -28,3 +28,30 @@ def test_the_library_is_built_without_torch(calls, monkeypatch, capsys):
     monkeypatch.setattr(B, "build_ops", needs_torch)
     assert B.build() == B.LIB and calls == ["library"]
     assert "torch is not installed" in capsys.readouterr().err
+
+
+def test_operators_are_built_again_for_another_torch(monkeypatch, tmp_path):
+    """An _ops.so that is newer than its sources is up to date only for the torch and Python it was built for."""
+    ops, runs = tmp_path / "_ops.so", []
+
+    def run(cmd, check):
+        runs.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            pass
+
+    monkeypatch.setattr(B, "OPS", str(ops))
+    monkeypatch.setattr(B, "OPS_STAMP", str(tmp_path / "made" / "_ops.stamp"), raising=False)
+    monkeypatch.setattr(B.subprocess, "run", run)
+    for _ in range(2):
+        B.build_ops()
+        assert len(runs) == 1 and ops.exists()
+    B.build_ops(force=True)
+    assert len(runs) == 2
+    version = B.metadata.version
+    monkeypatch.setattr(B.metadata, "version", lambda name: "9.9" if name == "torch" else version(name))
+    for _ in range(2):
+        B.build_ops()
+        assert len(runs) == 3
+    ops.unlink()
+    B.build_ops()
+    assert len(runs) == 4
