@@ -673,6 +673,41 @@ constexpr int kResTwo = 112 * 1024, kResOne = 224 * 1024;
 // backward (x and dy) 82 MB 62 against 82 us, 164 MB 145 against 125.
 constexpr long long kResMax = 100000000LL;
 
+// The largest cluster (16, 8, 4, 2 or 1 blocks, each with an SM's shared memory to itself) that a device can
+// place; 0: not asked yet.  A whole B200 places 16; a process that is given only some of its SMs may not.
+std::atomic<int> cluster_limits[64];
+
+// That of the current device, asked once; 16 where there is none, since sizes may be asked for without one.
+int cluster_limit() {
+    int dev = 0;
+    const bool there = cudaGetDevice(&dev) == cudaSuccess;
+    std::atomic<int>& known = cluster_limits[there ? dev & 63 : 0];
+    int n = known.load(std::memory_order_relaxed);
+    if (n) return n;
+    if (!there) {
+        cudaGetLastError();
+        return 16;
+    }
+    constexpr auto kern = k_norm_bwd_resident<float, 4, MH3A_ACT_SNAKE_BETA, true>;  // all take the same shared memory
+    for (n = allow_smem<kern>(kResOne, true) ? 16 : 1; n > 1; n /= 2) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(n);
+        cfg.blockDim = dim3(kResThreads);
+        cfg.dynamicSmemBytes = kResOne;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = n;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0) break;
+    }
+    cudaGetLastError();  // a size that the driver refuses is no error of the call
+    known.store(n, std::memory_order_relaxed);
+    return n;
+}
+
 FastDiv fast_div(unsigned d) { return FastDiv{d, (unsigned)(((1ull << 32) + d - 1) / d)}; }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -683,7 +718,7 @@ template <typename Extra>
 bool plan_resident(const NormArgs& a, int V, int e, int bytes_row, Extra extra, Resident* r) {
     const long long unit_l = (long long)a.D / gcd(a.D, V) * V;
     if (unit_l > kResThreads * V || a.B > 65535 || (long long)a.B * a.C * a.T > kResMax / bytes_row) return false;
-    const int unit = (int)unit_l, units = a.C / unit, most = kResThreads * V / unit;
+    const int unit = (int)unit_l, units = a.C / unit, most = kResThreads * V / unit, blocks = cluster_limit();
     for (int limit : {kResTwo, kResOne}) {
         for (int want : {128, 64}) {
             int k = 1;
@@ -696,9 +731,9 @@ bool plan_resident(const NormArgs& a, int V, int e, int bytes_row, Extra extra, 
             if (want == 128 && k > 1 && (long long)a.B * slabs * 8 < 2 * kSms && a.T >= 128) continue;
             auto bytes = [&](int s) { return (long long)((a.T + s - 1) / s) * W * bytes_row + extra(W, s); };
             int S = 1;
-            while (S < 16 && bytes(S) > limit) S *= 2;
+            while (S < blocks && bytes(S) > limit) S *= 2;
             if (bytes(S) > limit) continue;
-            while (S < 8 && (long long)a.B * slabs * S * 2 <= 2 * kSms && (a.T + 2 * S - 1) / (2 * S) >= 16) S *= 2;
+            while (S < std::min(8, blocks) && (long long)a.B * slabs * S * 2 <= 2 * kSms && (a.T + 2 * S - 1) / (2 * S) >= 16) S *= 2;
             *r = Resident{S, (a.T + S - 1) / S, W, slabs, (int)bytes(S), fast_div(kResThreads / (W / V)),
                           fast_div(W / V), fast_div(a.D), fast_div(a.D % V ? a.D : a.D / V)};
             return true;
