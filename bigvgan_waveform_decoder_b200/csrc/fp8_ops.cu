@@ -30,13 +30,15 @@ __device__ __forceinline__ void unpack16(uint4 q, float (&f)[16]) {
     }
 }
 
-// MR rows of x, two rows of w for each warp.  xs: the slab's quantised values times their scales,
-// [row][step][quarter][lane] of float4, so that a warp reads 512 consecutive bytes.  (q s is rounded
-// to fp32 before it is multiplied by the weights; the product's own rounding is of the same size.)
+// MR rows of x, two rows of w for each warp.  xs: the slab's quantised values, [row][step][quarter][lane] of
+// float4, so that a warp reads 512 consecutive bytes; ss: the scales of their blocks of 128 (8 lanes).  A lane's 16
+// products stand for themselves times two scales, the smaller of which is multiplied first: so nothing in between
+// leaves the range of fp32 that the result does not leave (x of 1e36 with weights of 1, say).
 template <typename T, typename O, int MR>
 __global__ void __launch_bounds__(kThreads) k_fp8_few_rows(const FewRowsArgs a, int x_vec) {
     constexpr int RW = 2;
     __shared__ float4 xs[MR][kSteps][4][32];
+    __shared__ float ss[MR][kSteps][4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n0 = (blockIdx.x * kWarps + warp) * RW;
     ptx::grid_dep_wait();
@@ -97,7 +99,8 @@ __global__ void __launch_bounds__(kThreads) k_fp8_few_rows(const FewRowsArgs a, 
             unpack16(make_uint4(q[0], q[1], q[2], q[3]), u);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                xs[m][t][i][lane] = make_float4(u[4 * i] * s, u[4 * i + 1] * s, u[4 * i + 2] * s, u[4 * i + 3] * s);
+                xs[m][t][i][lane] = make_float4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+            if (lane % 8 == 0) ss[m][t][lane / 8] = s;
         }
         __syncthreads();
         if (k0 + kSlab < a.K) fetch(next, k0 + kSlab);  // on their way while this slab is added up
@@ -127,8 +130,9 @@ __global__ void __launch_bounds__(kThreads) k_fp8_few_rows(const FewRowsArgs a, 
                         d[r] = fmaf(v.w, f[r][4 * i + 3], d[r]);
                     }
                 }
+                const float sx = ss[m][t][lane / 8];
 #pragma unroll
-                for (int r = 0; r < RW; ++r) acc[r][m] = fmaf(d[r], s[r], acc[r][m]);
+                for (int r = 0; r < RW; ++r) acc[r][m] = fmaf(d[r] * fminf(sx, s[r]), max_nan(sx, s[r]), acc[r][m]);
             }
         }
     }

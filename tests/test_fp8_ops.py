@@ -518,3 +518,19 @@ def test_gradients_are_not_lost_without_a_word(K):
     with pytest.raises(pkg.MH3AError, match="out cannot be given"):
         pkg.fp8_linear(req(x), w, sw, out=out)
     assert torch.equal(pkg.fp8_linear(x, w, sw, out=out), pkg.fp8_linear(x, w, sw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("M", (1, 2, 3, 4, 5, 200))
+def test_linear_of_large_and_small_values(M, dtype):
+    """Results within fp32's range, from operands whose products with the stored numbers (up to 448) or with each
+    other's scales are not."""
+    for up, down in ((36, 0), (30, -30), (-30, 30), (-18, -3), (37, -37)):
+        x = rand(M, 300, seed=M, spread=0.3) * 10.0 ** up
+        w = pkg.fp8_quantize(rand(80, 300, seed=1, spread=0.3) / 16 * 10.0 ** down, block_rows=128)
+        x = x.to(TYPES[dtype])
+        y = pkg.fp8_linear(x, *w)
+        assert bool(torch.isfinite(y).all())
+        xq, xs, _ = R.quantize(x, 1)
+        check_product(y, xq.float(), xs.float(), *w)
