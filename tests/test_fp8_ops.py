@@ -534,3 +534,23 @@ def test_linear_of_large_and_small_values(M, dtype):
         assert bool(torch.isfinite(y).all())
         xq, xs, _ = R.quantize(x, 1)
         check_product(y, xq.float(), xs.float(), *w)
+
+
+@pytest.mark.gpu
+def test_linear_of_rows_far_apart():
+    """Three rows more than 2^30 elements apart in a layer that is too large for the kernel of few rows, so that they are
+    quantised by a launch of its own; and the output's rows as far apart."""
+    far, N, K = (1 << 30) + 16, 16384, 1024
+    assert Bd.load().mh3a_fp8_linear_workspace(3, N, K) > 0
+    store = torch.empty(2 * far + N, device="cuda", dtype=torch.bfloat16)
+    x = store.as_strided((3, K), (far, 1))
+    x.copy_(rand(3, K, seed=1))
+    w, sw = pkg.fp8_quantize(rand(N, K, seed=2), block_rows=128)
+    want = pkg.fp8_linear(x.contiguous(), w, sw)
+    assert torch.equal(pkg.fp8_linear(x, w, sw), want)
+    xq, xs, _ = R.quantize(x, 1)
+    check_product(want, xq.float(), xs.float(), w, sw)
+    near = x.contiguous()
+    out = store.as_strided((3, N), (far, 1))
+    pkg.fp8_linear(near, w, sw, out=out)
+    assert torch.equal(out, want)

@@ -644,3 +644,107 @@ def test_inside_an_autograd_function():
     plain, mean, rstd = pkg.group_norm_act(x, 4, w, b, act="snake_beta", alpha=al, beta=be)
     want = pkg.group_norm_act_backward(dy, x, mean, rstd, 4, w, b, act="snake_beta", alpha=al, beta=be)
     assert torch.equal(y, plain) and all(torch.equal(t.grad, g) for t, g in zip(leaves, want))
+
+
+class Guarded:
+    """A buffer of exactly `shape` between guard values, on a 16-byte boundary."""
+
+    def __init__(self, shape, dtype, lead=64):
+        n = 1
+        for s in shape:
+            n *= s
+        self.all = torch.full((n + 2 * lead,), 7, dtype=dtype, device="cuda")
+        self.t = self.all[lead:lead + n].view(shape)
+        self.lead = lead
+
+    def ptr(self):
+        return self.t.data_ptr()
+
+    def whole(self):
+        return bool((self.all[:self.lead] == 7).all() and (self.all[-self.lead:] == 7).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths", (False, True), ids=("full", "ragged"))
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("shape", [(3, 301, 24, 3), (3, 301, 25, 5), (3, 301, 30, 2), (3, 301, 12, 4), (1, 5, 8, 1), (2, 1, 7, 7),
+                                   (3, 4001, 200, 8), (2, 700, 174, 3), (1, 3, 4104, 27)], ids=str)
+def test_guards_around_every_output_and_the_scratch(shape, dtype, lengths):
+    """Through the ABI, with scratch of exactly the size asked for: guard values around y, dx, the statistics, every
+    gradient and the scratch stay.  Resident and general forms, vectors of 1 to 8 channels."""
+    L = Bd.load()
+    B, T, Cn, G = shape
+    x, w, b, al, be = case(B, T, Cn, "snake_beta", dtype, seed=T)
+    dy = x.flip(1).contiguous()
+    n = torch.tensor([T, T // 2, 0][:B], dtype=torch.int32, device="cuda") if lengths else None
+    p = norm(dtype=("fp32", "fp16", "bf16").index(dtype), act=2, B=B, T=T, C=Cn, groups=G)
+    p.weight, p.bias, p.alpha, p.beta = (t.data_ptr() for t in (w, b, al, be))
+    p.lengths = n.data_ptr() if lengths else None
+    stream = torch.cuda.current_stream().cuda_stream
+    for aligned in (1, 0):
+        off = 1 - aligned  # an element off 16 bytes: narrower vectors
+        size = [L.mh3a_group_norm_act_workspace(C.byref(p), k, aligned) for k in (0, 1)]
+        ws = [Guarded((k,), torch.uint8) for k in size]
+        y, mean, rstd = Guarded(x.shape, x.dtype, 64 + off), Guarded((B, G), torch.float32), Guarded((B, G), torch.float32)
+        assert L.mh3a_group_norm_act(C.byref(p), x.data_ptr(), T * Cn, Cn, y.ptr(), mean.ptr(), rstd.ptr(), ws[0].ptr() if size[0] else None,
+                                     size[0], stream) == 0
+        dx, grads = Guarded(x.shape, x.dtype, 64 + off), [Guarded((Cn,), torch.float32) for _ in range(4)]
+        assert L.mh3a_group_norm_act_backward(C.byref(p), x.data_ptr(), T * Cn, Cn, dy.data_ptr(), T * Cn, Cn, mean.ptr(), rstd.ptr(),
+                                              dx.ptr(), *(g.ptr() for g in grads), ws[1].ptr() if size[1] else None, size[1], stream) == 0
+        for g in (y, mean, rstd, dx, *grads, *ws):
+            assert g.whole()
+        check_forward(x, G, w, b, "snake_beta", al, be, lengths=n, got=(y.t, mean.t, rstd.t))
+        check_backward(dy, x, mean.t, rstd.t, G, w, b, "snake_beta", al, be, lengths=n, got=(dx.t, *(g.t for g in grads)))
+
+
+GENERAL = [(3, 3001, 25, 5, 0), (3, 3001, 64, 8, 1), (2, 40, 30, 2, 0)]  # odd and even widths; parameters off 16 bytes
+
+
+def general_case(shape):
+    B, T, Cn, G, off = shape
+    x, *params = case(B, T, Cn, "snake_beta", "bf16", seed=T + Cn)
+    if off:
+        params = [torch.cat((p[:1], p))[1:] for p in params]
+    w, b, al, be = params
+    dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(2)).to(x.dtype).cuda()
+
+    def both(x, stream=None):
+        y, m, r = pkg.group_norm_act(x, G, w, b, act="snake_beta", alpha=al, beta=be, stream=stream)
+        return (y, m, r) + pkg.group_norm_act_backward(dy, x, m, r, G, w, b, act="snake_beta", alpha=al, beta=be, stream=stream)
+
+    return x, both
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", GENERAL, ids=str)
+def test_general_form_on_two_streams(shape):
+    """The launches of a call share scratch of their own, whatever another stream does."""
+    x, both = general_case(shape)
+    x2 = x.flip(0).contiguous()
+    first, second = both(x), both(x2)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    runs = [(both(x, s1), both(x2, s2.cuda_stream)) for _ in range(8)]
+    torch.cuda.synchronize()
+    for a, c in runs:
+        assert all(torch.equal(p, q) for p, q in zip(a, first))
+        assert all(torch.equal(p, q) for p, q in zip(c, second))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", GENERAL, ids=str)
+def test_general_form_captured_and_replayed(shape):
+    x, both = general_case(shape)
+    graphs, outs = [], []
+    for _ in range(2):  # two graphs with scratch of their own, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(both(x))
+        graphs.append(g)
+    x.copy_(x.flip(1).clone() * 1.5)
+    for k in (0, 1, 0):
+        graphs[k].replay()
+    torch.cuda.synchronize()
+    want = both(x)
+    for o in outs:
+        assert all(torch.equal(p, q) for p, q in zip(o, want))
