@@ -61,7 +61,9 @@ struct Cfg {
     static constexpr int kOther = kStaging + kScaleSlots * NT * 4 + 1024 + 512;
     static constexpr int kStages = std::min(8, (227 * 1024 - kOther) / kStageBytes);
     static constexpr int kSmem = kStages * kStageBytes + kOther;
-    // 128 columns of sums and two buffers of 32 do not fit an even share of the registers
+    // 128 columns of sums and two buffers of 32 do not fit an even share of the registers.  (With column scales
+    // the compiler spills a few values from 64 columns on: 48 to 92 bytes a thread with tiles of 64 and 128
+    // columns, 4 with 256.)
     static constexpr bool kSplitRegs = CW == 128;
 };
 
@@ -579,8 +581,10 @@ int launch(const MatmulArgs& m, cudaStream_t s) {
 
 template <typename O, bool WIDE>
 int launch_nt(const MatmulArgs& m, cudaStream_t s) {
-    // Rounds of tiles over the SMs, times what a round takes with tiles of that width (relative; measured
-    // at K = 2048: 9.4, 6.0, 3.7, 3.1 and 3.1 us, of one round 0.2 us less with 16 columns than with 32).
+    // Rounds of tiles over the SMs, times what a round takes with tiles of that width.  At K = 2048 a round takes
+    // 9.4, 6.0, 3.7, 3.1 and 3.1 us, of one round 0.2 us less with 16 columns than with 32; the weights below
+    // were fitted when the narrow tiles took longer, and choose what these times choose in all but one of 7936
+    // cases (128 to 12800 rows, 64 to 8192 columns).  K is left out: it stretches a round of every width.
     // Measured there, us with 256 / 128 / 64 / 32 / 16 columns: 64 x 2048: 10.6 / 7.4 / 5.9 / 5.5 / 5.3; 800 x
     // 1024: 11.9 / 8.2 / 6.8 / 9.0 / 14.5; 800 x 2048: 12.1 / 8.6 / 10.4 / 15.1 / 23.3; 2048 x 2048: 12.9 / 14.5 /
     // 17.8 / 24.6 / 44.6.

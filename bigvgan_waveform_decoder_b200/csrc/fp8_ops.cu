@@ -175,8 +175,8 @@ long long blocks(int n) { return (n + (long long)kBlock - 1) / kBlock; }
 
 // Whether a layer takes the kernel for few rows; its multiplications are the CUDA cores', so the tensor
 // cores overtake it where there are many.  Measured, us, this kernel against quantisation and product
-// (columns x K): 1 row 2048 x 2048 3.4 / 6.3, 4096 x 4096 6.7 / 9.7, 8192 x 8192 25.7 / 16.7; 2 rows 4096 x 4096
-// 7.7 / 9.8; 3 rows 4096 x 4096 11.3 / 9.8; 4 rows 2048 x 2048 5.0 / 6.6.
+// (columns x K): 1 row 2048 x 2048 3.3 / 6.3, 4096 x 4096 6.7 / 9.7, 8192 x 8192 25.7 / 16.7; 2 rows 4096 x 4096
+// 8.0 / 9.8; 3 rows 4096 x 4096 11.3 / 9.8; 4 rows 2048 x 2048 4.9 / 6.6.
 bool few_rows(int M, int N, int K) { return M <= MH3A_FP8_FEW_ROWS && (long long)M * N * K <= 40LL << 20; }
 
 // Layout of mh3a_fp8_linear's scratch: x quantised, then its scales.

@@ -137,8 +137,10 @@ __device__ __forceinline__ float clamp_nan(float v, float c) {
 // 1.5 2^23, right for |theta| below 2^22 pi; farther out fp32 leaves theta no fraction of a period, and
 // the clamp keeps the result a sine.
 //
-// 16-bit tensors: the hardware sine, whose 2^-21 absolute error is far below their rounding; its
-// argument loses |theta| 2^-24 as the product itself does, so a reduction first would gain nothing.
+// 16-bit tensors: the hardware sine, whose 2^-21 absolute error is far below the rounding of y and dx; its
+// argument loses |theta| 2^-24 as the product itself does, so a reduction first would gain nothing.  In the
+// parameters' gradients, fp32 sums, it does show: off by 2.3 to 5.5 x 10^-7 of their size where the series
+// gives 1.1 to 2.4 x 10^-7 (1 to 160000 rows), of inputs that are rounded to 2^-9 or 2^-12 themselves.
 template <bool PRECISE, bool COS>
 __device__ __forceinline__ void sin_cos_mod_pi(float2 alpha, float2 u, float2* sn, float2* cs) {
     const float2 v = __fmul2_rn(alpha, u);
@@ -177,6 +179,7 @@ __device__ __forceinline__ float ex2_ftz(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// (Also 1 / (beta + 1e-9), for all types: within one unit in the last place, where a division is within half.)
 __device__ __forceinline__ float rcp_ftz(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -352,7 +352,12 @@ MH3A_API size_t mh3a_group_norm_act_workspace(const mh3a_norm* p, int backward, 
  * x: device, channels adjacent, item b and row t at x + b x_batch_stride + t x_row_stride
  * elements (strides >= 0; 0 repeats an item or a row).  y: device [B, T, C], contiguous, must not
  * overlap an input.  mean, rstd: device [B, groups], what the backward pass needs.  An item of no valid
- * rows has mean 0 and var 0.  All arithmetic is fp32 (combining partial statistics: fp64), rounded once to the type of y.
+ * rows has mean 0 and var 0.
+ * Arithmetic is fp32 (combining partial statistics: fp64), rounded once to the type of y.  For 16-bit x
+ * the activation takes the hardware's approximations: sine and cosine to 2^-21 (absolute, and 2^-24 of the
+ * angle more), exponential and reciprocal to a few units of 2^-24; y is off by its own rounding all the same.  For
+ * fp32 x they are accurate to a few units of 2^-24, and 1 / (beta + 1e-9) comes from the hardware's reciprocal
+ * (within one unit in the last place) for all types.
  * `workspace`: device, 16-byte aligned, at least mh3a_group_norm_act_workspace(p, 0, aligned) bytes
  * (NULL where that is 0).
  * Errors: MH3A_ERR_INVALID_ARG (NULL p, x, y, mean or rstd; unknown dtype or act; alpha or beta
@@ -367,7 +372,9 @@ MH3A_API mh3a_status mh3a_group_norm_act(const mh3a_norm* p, const void* x, long
  * rstd are the forward pass's.  dx: device [B, T, C], contiguous, must not overlap an input.
  * dweight, dbias, dalpha, dbeta: device [C] fp32, summed over all items and valid rows; each may
  * be NULL when it is not wanted (dalpha and dbeta must be NULL unless act is
- * MH3A_ACT_SNAKE_BETA).  Errors as mh3a_group_norm_act. */
+ * MH3A_ACT_SNAKE_BETA).  Arithmetic as above: with 16-bit x and SnakeBeta the hardware's sine shows in
+ * these fp32 sums, 2 to 5 x 10^-7 of their size against 1 to 3 x 10^-7 for fp32 x.  Errors as
+ * mh3a_group_norm_act. */
 MH3A_API mh3a_status mh3a_group_norm_act_backward(const mh3a_norm* p, const void* x, long long x_batch_stride,
                                                   long long x_row_stride, const void* dy,
                                                   long long dy_batch_stride, long long dy_row_stride,
@@ -398,7 +405,9 @@ MH3A_API mh3a_status mh3a_fp8_quantize(const void* x, int dtype, int rows, int c
 
 /* out[m, n] = sum_k a[m, k] b[n, k] + bias[n], a [M, K] with block_rows 1 and b [N, K] with
  * b_block_rows 1 or 128, both as above.  The products of a block are added on the tensor cores, the
- * blocks scaled and added in fp32; the sum is rounded once to out_dtype (mh3a_dtype).  bias: device
+ * blocks scaled and added in fp32; the sum is rounded once to out_dtype (mh3a_dtype).  A block's two scales
+ * are multiplied with each other or one after the other, so where their product leaves fp32's normal numbers
+ * (below 2^-126, 2^128 and above) the block's part of the sum loses bits, or is 0, infinite or NaN.  bias: device
  * fp32 [N] or NULL.  out: device, columns adjacent, rows out_stride elements apart; must not overlap
  * an input.  Errors: MH3A_ERR_INVALID_ARG (NULL or misaligned pointers, unknown dtype,
  * b_block_rows other than 1 or 128, a stride below the row's length, an operand's stride not a
