@@ -701,9 +701,9 @@ int cluster_limit() {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0) break;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess) cudaGetLastError();  // no error of the call
+        else if (clusters > 0) break;
     }
-    cudaGetLastError();  // a size that the driver refuses is no error of the call
     known.store(n, std::memory_order_relaxed);
     return n;
 }

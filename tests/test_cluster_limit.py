@@ -2,6 +2,7 @@
 import ctypes as C
 import os
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -82,3 +83,28 @@ def test_results_with_smaller_clusters(limited, limit, shape, dtype):
     assert limited.mh3a_group_norm_act_backward(C.byref(p), x.data_ptr(), T * Cn, Cn, dy.data_ptr(), T * Cn, Cn, mean.data_ptr(),
                                                 rstd.data_ptr(), dx.data_ptr(), *(t.data_ptr() for t in g), ws.data_ptr(), n, stream) == 0
     check_backward(dy, x, mean, rstd, G, w, b, "snake_beta", al, be, got=(dx, *g))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", ("norm", "linear"))
+def test_the_first_call_of_a_process_may_be_captured(op):
+    """What a device is asked for once, and what is set up once for a kernel, does not get in a capture's way."""
+    code = f"""
+import torch, bigvgan_waveform_decoder_b200 as pkg
+x = torch.randn(2, 900, 64, device="cuda")
+q = torch.ones(64, 64, device="cuda").to(torch.float8_e4m3fn)
+s = torch.ones(1, 1, device="cuda")
+def call():
+    if "{op}" == "norm":
+        y, m, r = pkg.group_norm_act(x, 4)
+        return y, pkg.group_norm_act_backward(x, x, m, r, 4)[0]
+    return pkg.fp8_linear(x[0], q, s), pkg.fp8_linear(x[0, :1], q, s)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    outs = call()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(outs, call()))
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=B.ROOT, timeout=300)
